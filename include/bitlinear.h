@@ -60,7 +60,8 @@ typedef enum {
     BITLINEAR_ERR_SCRATCH_LIMIT = 8, /* problem too large for the library's static scratch */
     BITLINEAR_ERR_HOST = 9,      /* a host allocation failed */
     BITLINEAR_ERR_IO = 10,       /* a file could not be opened, written or renamed */
-    BITLINEAR_ERR_FORMAT = 11    /* not a valid packed-weight file (header, size or checksum) */
+    BITLINEAR_ERR_FORMAT = 11,   /* not a valid packed-weight file (header, size or checksum) */
+    BITLINEAR_ERR_INDEX = 12     /* an index that device memory held was out of range */
 } bitlinear_status;
 
 typedef enum {
@@ -496,14 +497,130 @@ int bitlinear_forward_noalloc(const void *x_dev, bitlinear_dtype xdt, int64_t M,
                               int64_t K, const void *packed_dev, float gamma,
                               int64_t N, void *y_dev, void *cuda_stream);
 
+/* --------------------------------------------- attention on a paged cache */
+
+/* The attention half of a decoder layer, between the q/k/v projections and
+ * the o projection: rotary positions ("Microsoft Releases BitNet b1.58 2B4T",
+ * section "Under the Hood") and causal attention with shared key heads over a
+ * cache of keys and values that is kept in pages. Activations and cache are
+ * bf16, like the outputs of the projections.
+ *
+ * A cache is two buffers [pages][kv_heads][page][head_dim] (bf16, 16-byte
+ * aligned): a page holds `page` consecutive positions of one sequence.
+ * head_dim is 64 or 128, page 16, 32, 64, 128 or 256. */
+typedef struct {
+    void *k_dev, *v_dev;
+    int64_t pages, kv_heads, page, head_dim;
+} bitlinear_kv_cache;
+
+/* The sequences of one step, all arrays in device memory (the host never
+ * reads them, so a captured graph follows their values):
+ *   q_start_dev    [seqs + 1] non-decreasing: sequence s owns the query rows
+ *                  q_start[s] .. q_start[s + 1] - 1; none is allowed. Rows in
+ *                  front of q_start[0] and behind q_start[seqs] (a batch padded
+ *                  to a captured size) belong to no sequence and stay as they
+ *                  are.
+ *   kv_len_dev     [seqs] tokens of the sequence in the cache, its new ones
+ *                  included: row i of a sequence of n rows stands at position
+ *                  kv_len - n + i. Rows at negative positions see no key.
+ *   page_table_dev [seqs][table_cols]: position j of sequence s is slot
+ *                  j % page of page page_table[s][j / page]. Columns behind
+ *                  the sequence's last page (and in front of its window) are
+ *                  not read. Sequences may share pages that no call writes.
+ * At most 16384 sequences. A value that points outside the rows, the table or
+ * the cache is never used for an access: bitlinear_get_fault reports it
+ * (BITLINEAR_ERR_INDEX), a key on such a page counts as zeros, a token that
+ * belongs there is not stored, and the results of that sequence are otherwise
+ * unspecified. */
+typedef struct {
+    const int32_t *q_start_dev, *kv_len_dev, *page_table_dev;
+    int64_t seqs, table_cols;
+} bitlinear_seqs;
+
+/* Rotates the queries and keys of the step's tokens by their positions,
+ * optionally RMS-normalising every head first, and stores the keys and the
+ * values in their pages: one launch.
+ *   q_dev, k_dev, v_dev  [in] tokens rows of q_heads (k, v: cache->kv_heads)
+ *                  heads of head_dim bf16, row t at element t * stride; strides
+ *                  are multiples of 8, so the three may be parts of one wider
+ *                  buffer; 16-byte aligned
+ *   tokens   [in]  rows that exist (at least q_start[seqs])
+ *   inv_freq_dev [in] [head_dim / 2] fp32 frequencies f; the angle of pair i at
+ *                  position p is p * f_i, taken in double
+ *   interleaved [in] 0: pair i is channels i and i + head_dim / 2;
+ *                  1: channels 2 i and 2 i + 1
+ *   q_gain_dev, k_gain_dev [in] [head_dim] fp32 gains of the per-head
+ *                  normalisation x * g / sqrt(mean x^2 + norm_eps) of the
+ *                  queries and of the keys, each NULL for none
+ *   norm_eps [in]  finite and > 0 when a gain is given
+ *   q_out_dev [out] the rotated queries, q_out_stride likewise; may be q_dev
+ *                  (with the same stride)
+ * Everything between load and store is fp32, rounded once to bf16. Tokens at
+ * negative positions are skipped. Two rows must not have the same place in the
+ * cache. */
+int bitlinear_rope_append(const void *q_dev, int64_t q_stride,
+                          const void *k_dev, int64_t k_stride,
+                          const void *v_dev, int64_t v_stride, int64_t tokens,
+                          int64_t q_heads, const bitlinear_kv_cache *cache,
+                          const bitlinear_seqs *seqs,
+                          const float *inv_freq_dev, int interleaved,
+                          const float *q_gain_dev, const float *k_gain_dev,
+                          float norm_eps, void *q_out_dev,
+                          int64_t q_out_stride, void *cuda_stream);
+
+/* Workspace bytes of bitlinear_paged_attention for `tokens` query rows: room
+ * for the partial sums of keys that are split between workers. It depends on
+ * no length, so one workspace serves every step of a shape. SIZE_MAX for
+ * shapes the call refuses. */
+size_t bitlinear_workspace_bytes_attention(int64_t tokens, int64_t seqs,
+                                           int64_t q_heads, int64_t kv_heads,
+                                           int64_t head_dim);
+
+/* Attention of every sequence's new tokens to its keys in the cache (its new
+ * ones included: append first):
+ *   y_t = sum_j softmax_j(scale * q_t . k_j) v_j,   p_t - window < j <= p_t
+ * (no lower limit when window is 0). Query head h uses key head
+ * h / (q_heads / kv_heads). Single tokens, drafted tokens, chunks of prompts
+ * and whole prompts are the same call and may be mixed.
+ *   q_dev, q_stride, tokens, q_heads, cache, seqs [in] as for
+ *                  bitlinear_rope_append; q_heads a multiple of kv_heads
+ *   scale    [in]  finite and > 0
+ *   window   [in]  keys that a token sees, itself included; 0: all before it
+ *   max_q_len [in] the largest number of rows of any sequence when the host
+ *                  knows it, or 0. A hint that chooses the kernels: a smaller
+ *                  value costs speed, never correctness
+ *   y_dev, y_stride [out] rows of q_heads * head_dim bf16, 16-byte aligned,
+ *                  stride a multiple of 8. Rows that see no key are zero; rows
+ *                  of no sequence stay as they are. May not overlap q_dev
+ *   lse_dev_or_null [out, optional] [tokens][q_heads] fp32: the natural
+ *                  logarithm of sum_j exp(scale * q_t . k_j), -inf for a row
+ *                  without keys
+ *   workspace_dev, workspace_bytes [in] bitlinear_workspace_bytes_attention
+ *                  bytes, 256-byte aligned, no initialisation needed; not
+ *                  shared with a call that may run at the same time
+ * Scores, maxima, sums and the output are fp32; the weights of the sum over
+ * the values are rounded to bf16 for the tensor cores. Queries, and keys and
+ * values at the positions that a sequence's rows see, are finite; the other
+ * slots of its pages may hold anything. Repeated calls give the same bits. */
+int bitlinear_paged_attention(const void *q_dev, int64_t q_stride,
+                              int64_t tokens, int64_t q_heads,
+                              const bitlinear_kv_cache *cache,
+                              const bitlinear_seqs *seqs, float scale,
+                              int64_t window, int64_t max_q_len, void *y_dev,
+                              int64_t y_stride, float *lse_dev_or_null,
+                              void *workspace_dev, size_t workspace_bytes,
+                              void *cuda_stream);
+
 /* ------------------------------------------------------------- diagnostics */
 
-/* Device-side fault word. Every bounded wait in the tensor-core GEMM gives
- * up after a time limit, records a nonzero code here and lets the kernel
- * return instead of hanging. This call synchronises cuda_stream, stores the
- * word in *fault_out (0 = none) and clears it. Returns BITLINEAR_ERR_TIMEOUT
- * when the word was set, BITLINEAR_ERR_CUDA when the synchronisation failed,
- * BITLINEAR_OK otherwise. */
+/* Device-side fault word. Every bounded wait in a kernel gives up after a
+ * time limit, records bit 0 here and lets the kernel return instead of
+ * hanging; a kernel that finds an index in device memory (bitlinear_seqs) out
+ * of range records bit 1 and makes no access with it. This call synchronises
+ * cuda_stream, stores the word in *fault_out (0 = none) and clears it. Returns
+ * BITLINEAR_ERR_TIMEOUT when bit 0 was set, BITLINEAR_ERR_INDEX when bit 1
+ * alone was, BITLINEAR_ERR_CUDA when the synchronisation failed, BITLINEAR_OK
+ * otherwise. */
 int bitlinear_get_fault(int *fault_out, void *cuda_stream);
 
 /* Human-readable name of a bitlinear_status. Never NULL. */

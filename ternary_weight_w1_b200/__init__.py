@@ -29,6 +29,7 @@ BITLINEAR_ERR_SCRATCH_LIMIT = 8
 BITLINEAR_ERR_HOST = 9
 BITLINEAR_ERR_IO = 10
 BITLINEAR_ERR_FORMAT = 11
+BITLINEAR_ERR_INDEX = 12
 BITLINEAR_STATIC_SCRATCH_BYTES = 16 << 20
 
 BITLINEAR_BF16 = 0
@@ -70,6 +71,9 @@ EXPORTS = (
     "bitlinear_forward_grouped_rmsnorm",
     "bitlinear_workspace_bytes_ffn",
     "bitlinear_ffn_forward",
+    "bitlinear_rope_append",
+    "bitlinear_workspace_bytes_attention",
+    "bitlinear_paged_attention",
 )
 
 
@@ -77,6 +81,19 @@ class _Problem(ctypes.Structure):
     _fields_ = [("x_dev", ctypes.c_void_p), ("M", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("N", ctypes.c_int64), ("packed_dev", ctypes.c_void_p),
                 ("gamma", ctypes.c_float), ("y_dev", ctypes.c_void_p)]
+
+
+class _KVCache(ctypes.Structure):
+    _fields_ = [("k_dev", ctypes.c_void_p), ("v_dev", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("kv_heads", ctypes.c_int64),
+                ("page", ctypes.c_int64), ("head_dim", ctypes.c_int64)]
+
+
+class _Seqs(ctypes.Structure):
+    _fields_ = [("q_start_dev", ctypes.c_void_p), ("kv_len_dev", ctypes.c_void_p),
+                ("page_table_dev", ctypes.c_void_p), ("seqs", ctypes.c_int64),
+                ("table_cols", ctypes.c_int64)]
+
 
 _lib = None
 
@@ -153,6 +170,14 @@ def lib() -> ctypes.CDLL:
         L.bitlinear_ffn_forward.restype = ctypes.c_int
         L.bitlinear_ffn_forward.argtypes = [p, ctypes.c_int, i64, i64, i64, p, f32, p, f32, p,
                                             f32, p, p, p, f32, p, p, p, sz, p, p, p]
+        L.bitlinear_rope_append.restype = ctypes.c_int
+        L.bitlinear_rope_append.argtypes = [p, i64, p, i64, p, i64, i64, i64, p, p, p,
+                                            ctypes.c_int, p, p, f32, p, i64, p]
+        L.bitlinear_workspace_bytes_attention.restype = sz
+        L.bitlinear_workspace_bytes_attention.argtypes = [i64, i64, i64, i64, i64]
+        L.bitlinear_paged_attention.restype = ctypes.c_int
+        L.bitlinear_paged_attention.argtypes = [p, i64, i64, i64, p, p, f32, i64, i64, p, i64, p,
+                                                p, sz, p]
         L.bitlinear_get_fault.restype = ctypes.c_int
         L.bitlinear_get_fault.argtypes = [p, p]
         L.bitlinear_status_string.restype = ctypes.c_char_p
@@ -186,7 +211,8 @@ class _Args:
     def __init__(self):
         self.cur = None
 
-    def ptr(self, t, name: str, dtype=None, shape=None, min_numel: int = 0) -> int | None:
+    def ptr(self, t, name: str, dtype=None, shape=None, min_numel: int = 0,
+            contiguous: bool = True) -> int | None:
         if t is None:
             return None
         d = t.get_device()
@@ -197,7 +223,7 @@ class _Args:
             self.cur = torch.cuda.current_device()
         if d != self.cur:
             raise ValueError(f"{name} is on cuda:{d}, the current device is cuda:{self.cur}")
-        if not t.is_contiguous():
+        if contiguous and not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         if dtype is not None and t.dtype != dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -206,6 +232,29 @@ class _Args:
         if min_numel and t.numel() < min_numel:
             raise ValueError(f"{name} holds {t.numel()} elements, {min_numel} needed")
         return t.data_ptr()
+
+    def rows(self, t, name: str, heads: int | None, head_dim: int):
+        """(address, row stride, heads) of a bf16 tensor of rows of whole
+        heads, [T][heads * head_dim] or [T][heads][head_dim]: its rows may be
+        any distance apart (a part of a wider tensor), a row is contiguous."""
+        import torch
+        if t.dim() == 3:
+            ok = t.shape[2] == head_dim and (t.stride(2) == 1 and t.stride(1) == head_dim
+                                             or t.numel() == 0 or t.shape[1] == 1
+                                             and t.stride(2) == 1)
+            width = t.shape[1] * head_dim
+        else:
+            ok = t.dim() == 2 and t.shape[1] % head_dim == 0 and (t.stride(1) == 1
+                                                                  or t.numel() == 0)
+            width = t.shape[1] if t.dim() == 2 else 0
+        if not ok or width == 0 or (heads is not None and width != heads * head_dim):
+            raise ValueError(f"{name} must be [T][heads * {head_dim}] or [T][heads][{head_dim}]"
+                             + (f" with {heads} heads" if heads is not None else "")
+                             + f" and contiguous in a row, got {tuple(t.shape)} with strides "
+                             f"{tuple(t.stride())}")
+        stride = t.stride(0) if t.shape[0] > 1 else width
+        return self.ptr(t[:0] if t.numel() == 0 else t, name, torch.bfloat16,
+                        contiguous=False), stride, width // head_dim
 
     def packed(self, packed, N: int, K: int) -> int | None:
         import torch
@@ -508,6 +557,126 @@ def _ffn_width(packed, K: int) -> int:
     """F of an F x K packed matrix whose F is a multiple of 16 (as every d_ff
     the feed-forward call accepts, a multiple of 128, is)."""
     return packed.numel() // (K // 4)
+
+
+# ------------------------------------------------- attention on a paged cache
+
+def _paged(a: _Args, k_cache, v_cache, q_start, kv_len, page_table):
+    """The cache and sequence descriptors of one call (k_cache and v_cache
+    [pages][kv_heads][page][head_dim] bf16; q_start [S + 1], kv_len [S] and
+    page_table [S][columns] int32)."""
+    import torch
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [pages][kv_heads][page][head_dim], got "
+                         f"{tuple(k_cache.shape)}")
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table must be [S][columns], got {tuple(page_table.shape)}")
+    S, cols = page_table.shape
+    pages, kv_heads, page, head_dim = k_cache.shape
+    if head_dim not in (64, 128):
+        raise BitLinearError(BITLINEAR_ERR_SHAPE, f"k_cache with head_dim {head_dim}")
+    cache = _KVCache(a.ptr(k_cache, "k_cache", torch.bfloat16),
+                     a.ptr(v_cache, "v_cache", torch.bfloat16, k_cache.shape),
+                     pages, kv_heads, page, head_dim)
+    seqs = _Seqs(a.ptr(q_start, "q_start", torch.int32, (S + 1,)),
+                 a.ptr(kv_len, "kv_len", torch.int32, (S,)),
+                 a.ptr(page_table, "page_table", torch.int32), S, cols)
+    return cache, seqs
+
+
+def _new(t, stream, shape=None, dtype=None):
+    """A tensor that the call allocates: like ``t``, kept from reuse until the
+    work on ``stream`` is done when that is not the current stream."""
+    import torch
+    out = torch.empty(t.shape if shape is None else shape,
+                      dtype=t.dtype if dtype is None else dtype, device=t.device)
+    if stream is not None and stream != torch.cuda.current_stream():
+        stream.wait_stream(torch.cuda.current_stream())   # what used the memory before
+        out.record_stream(stream)
+    return out
+
+
+def bitlinear_rope_append(q, k, v, k_cache, v_cache, q_start, kv_len, page_table, inv_freq,
+                          q_out=None, q_gain=None, k_gain=None, eps: float = RMSNORM_EPS,
+                          interleaved: bool = False, stream=None):
+    """Rotates the step's queries and keys by their positions (after an
+    optional RMSNorm of every head with the fp32 gains ``q_gain`` /
+    ``k_gain`` [head_dim]) and stores the keys and the values ``v`` in the
+    pages of their sequences, in one launch. ``q`` [T][heads * head_dim] or
+    [T][heads][head_dim], ``k`` and ``v`` likewise with the cache's heads, all
+    bf16, rows any multiple of 8 elements apart; ``inv_freq`` [head_dim / 2]
+    fp32. Row i of sequence s (rows q_start[s] .. q_start[s + 1]) stands at
+    position kv_len[s] - its rows + i. Returns the rotated queries (``q_out``,
+    which may be ``q``; rows of no sequence are not written)."""
+    a = _Args()
+    import torch
+    cache, seqs = _paged(a, k_cache, v_cache, q_start, kv_len, page_table)
+    D = cache.head_dim
+    qp, qs, heads = a.rows(q, "q", None, D)
+    kp, ks, _ = a.rows(k, "k", cache.kv_heads, D)
+    vp, vs, _ = a.rows(v, "v", cache.kv_heads, D)
+    if k.shape[0] != q.shape[0] or v.shape[0] != q.shape[0]:
+        raise ValueError(f"q, k and v must have the same rows, got {q.shape[0]}, {k.shape[0]}, "
+                         f"{v.shape[0]}")
+    if q_out is None:
+        q_out = _new(q, stream)
+    op, os_, _ = a.rows(q_out, "q_out", heads, D)
+    if q_out.shape[0] != q.shape[0]:
+        raise ValueError(f"q_out must have {q.shape[0]} rows, got {q_out.shape[0]}")
+    _check(lib().bitlinear_rope_append(
+               qp, qs, kp, ks, vp, vs, q.shape[0], heads, ctypes.addressof(cache),
+               ctypes.addressof(seqs), a.ptr(inv_freq, "inv_freq", torch.float32, (D // 2,)),
+               1 if interleaved else 0, a.ptr(q_gain, "q_gain", torch.float32, (D,)),
+               a.ptr(k_gain, "k_gain", torch.float32, (D,)), float(eps), op, os_,
+               _stream(stream)),
+           "bitlinear_rope_append")
+    return q_out
+
+
+def bitlinear_workspace_bytes_attention(tokens: int, seqs: int, q_heads: int, kv_heads: int,
+                                        head_dim: int) -> int:
+    return int(lib().bitlinear_workspace_bytes_attention(tokens, seqs, q_heads, kv_heads,
+                                                         head_dim))
+
+
+def bitlinear_paged_attention(q, k_cache, v_cache, q_start, kv_len, page_table, scale=None,
+                              window: int = 0, max_q_len: int | None = None, y=None, lse=None,
+                              workspace=None, stream=None):
+    """Causal attention of every sequence's new tokens to its keys in the paged
+    cache (``bitlinear_rope_append`` stores the new ones first): single tokens,
+    drafted tokens, chunks of prompts and whole prompts, also mixed. Arguments
+    as there; ``scale`` defaults to head_dim ** -0.5, ``window`` > 0 limits a
+    token to its last ``window`` keys, ``max_q_len`` is the longest sequence's
+    rows when the host knows it (it chooses the kernels). ``lse`` (fp32
+    [T][heads]) optionally receives the log-sum-exp of every row's scores.
+    ``workspace`` is a device uint8 tensor of
+    ``bitlinear_workspace_bytes_attention`` bytes (allocated here when
+    omitted). Returns ``y`` (bf16, shaped like ``q``; rows that see no key are
+    zero, rows of no sequence are not written)."""
+    a = _Args()
+    import torch
+    cache, seqs = _paged(a, k_cache, v_cache, q_start, kv_len, page_table)
+    D = cache.head_dim
+    qp, qs, heads = a.rows(q, "q", None, D)
+    T = q.shape[0]
+    if y is None:
+        y = _new(q, stream)
+    yp, ys, _ = a.rows(y, "y", heads, D)
+    if y.shape[0] != T:
+        raise ValueError(f"y must have {T} rows, got {y.shape[0]}")
+    need = bitlinear_workspace_bytes_attention(T, seqs.seqs, heads, cache.kv_heads, D)
+    if need == ctypes.c_size_t(-1).value:
+        raise BitLinearError(BITLINEAR_ERR_SHAPE, "bitlinear_workspace_bytes_attention")
+    if workspace is None and need > 0:
+        workspace = _new(q, stream, (need,), torch.uint8)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().bitlinear_paged_attention(
+               qp, qs, T, heads, ctypes.addressof(cache), ctypes.addressof(seqs),
+               float(D ** -0.5 if scale is None else scale), int(window),
+               int(max_q_len or 0), yp, ys, a.ptr(lse, "lse", torch.float32, (T, heads)),
+               a.ptr(workspace, "workspace"), ws_bytes, _stream(stream)),
+           "bitlinear_paged_attention")
+    return y
 
 
 def bitlinear_get_fault(stream=None) -> tuple[int, int]:

@@ -1,0 +1,308 @@
+// Host side of the operators on the paged key/value cache: argument checks,
+// kernel choice and launches. Included by bitlinear.cu after its launch
+// helpers; the C ABI functions are declared in include/bitlinear.h.
+#pragma once
+
+namespace {
+
+constexpr int kAttnMaxGrid = 192;                    // blocks of a launch; the parts are sized by it
+constexpr int64_t kAttnMaxSeqs = 32 * paged::MAX_GROUPS;
+constexpr int64_t kAttnMaxKeys = int64_t(1) << 30;   // page slots of a sequence
+constexpr int64_t kAttnMaxRows = int64_t(1) << 30;   // tokens * query heads
+
+// Rows of the queries or of the tensors beside them: a stride that keeps every
+// row 16-byte aligned and apart from the next.
+int check_rows(const void *p, int64_t stride, int64_t width)
+{
+    if (p == nullptr)
+        return BITLINEAR_ERR_ARG;
+    if (stride < width)
+        return BITLINEAR_ERR_SHAPE;
+    if (!aligned(p, 16) || stride % 8 != 0)
+        return BITLINEAR_ERR_ALIGN;
+    return BITLINEAR_OK;
+}
+
+// The shape checks of a cache and its sequences, without the pointers.
+int check_paged_shape(int64_t tokens, int64_t seqs, int64_t q_heads, int64_t kv_heads,
+                      int64_t head_dim)
+{
+    if (tokens < 0 || seqs < 0 || q_heads < 1 || kv_heads < 1)
+        return BITLINEAR_ERR_ARG;
+    if ((head_dim != 64 && head_dim != 128) || q_heads % kv_heads != 0 || q_heads > 65536 ||
+        tokens > kAttnMaxRows / q_heads || seqs > kAttnMaxSeqs)
+        return BITLINEAR_ERR_SHAPE;
+    return BITLINEAR_OK;
+}
+
+int check_paged(int64_t tokens, int64_t q_heads, const bitlinear_kv_cache *c,
+                const bitlinear_seqs *s, bool *empty)
+{
+    *empty = false;
+    if (c == nullptr || s == nullptr || c->pages < 1 || s->table_cols < 1)
+        return BITLINEAR_ERR_ARG;
+    int rc = check_paged_shape(tokens, s->seqs, q_heads, c->kv_heads, c->head_dim);
+    if (rc != BITLINEAR_OK)
+        return rc;
+    if (c->page < 16 || c->page > 256 || (c->page & (c->page - 1)) != 0 ||
+        s->table_cols > kAttnMaxKeys / c->page ||
+        c->pages > (INT_MAX - 512) / (c->kv_heads * c->page))
+        return BITLINEAR_ERR_SHAPE;
+    if (tokens == 0 || s->seqs == 0) {
+        *empty = true;
+        return BITLINEAR_OK;
+    }
+    if (c->k_dev == nullptr || c->v_dev == nullptr || s->q_start_dev == nullptr ||
+        s->kv_len_dev == nullptr || s->page_table_dev == nullptr)
+        return BITLINEAR_ERR_ARG;
+    if (!aligned(c->k_dev, 16) || !aligned(c->v_dev, 16) || !aligned(s->q_start_dev, 4) ||
+        !aligned(s->kv_len_dev, 4) || !aligned(s->page_table_dev, 4))
+        return BITLINEAR_ERR_ALIGN;
+    return BITLINEAR_OK;
+}
+
+int log2_of(int64_t v)
+{
+    int n = 0;
+    while ((int64_t(1) << n) < v)
+        ++n;
+    return n;
+}
+
+paged::Seqs device_seqs(const bitlinear_kv_cache &c, const bitlinear_seqs &s, int64_t tokens)
+{
+    return paged::Seqs{s.q_start_dev,
+                       s.kv_len_dev,
+                       s.page_table_dev,
+                       static_cast<int>(s.seqs),
+                       static_cast<int>(s.table_cols),
+                       static_cast<int>(tokens),
+                       log2_of(c.page),
+                       static_cast<int>(c.pages)};
+}
+
+// ------------------------------------------------------------ rope + append
+
+template <int D>
+cudaError_t launch_rope(const rope::Params &p, bool interleaved, int grid, cudaStream_t st)
+{
+    return interleaved
+               ? launch(rope::rope_append_kernel<D, true>, dim3(grid), dim3(rope::THREADS), 0, st, p)
+               : launch(rope::rope_append_kernel<D, false>, dim3(grid), dim3(rope::THREADS), 0, st,
+                        p);
+}
+
+// ---------------------------------------------------------------- attention
+
+// A cache as a 2-D tensor {head_dim, pages * kv_heads * page} of bf16, boxed
+// as {64 channels, box_rows} with the 128-byte swizzle: one box is a run of
+// box_rows slots of one page and key head, 64 channels of each.
+bool make_map_cache(CUtensorMap *map, const void *ptr, const bitlinear_kv_cache &c,
+                    uint32_t box_rows)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr)
+        return false;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(c.head_dim),
+                                static_cast<cuuint64_t>(c.pages * c.kv_heads * c.page)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(c.head_dim) * 2};
+    const cuuint32_t box[2] = {64, box_rows};
+    const cuuint32_t estride[2] = {1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(ptr), dims, strides,
+              box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// The parts of one attention kernel inside the workspace: headers, maxima and
+// sums, accumulators, for two slots a worker.
+size_t parts_layout(int64_t workers, int64_t row_cap, int64_t head_dim, char *base,
+                    paged::Parts *out)
+{
+    const size_t hb = round_up(static_cast<size_t>(2 * workers) * sizeof(paged::PartHeader), 256);
+    const size_t mb = round_up(static_cast<size_t>(2 * workers * row_cap) * sizeof(float2), 256);
+    const size_t ob = round_up(static_cast<size_t>(2 * workers * row_cap * head_dim) * 4, 256);
+    if (out != nullptr) {
+        out->headers = reinterpret_cast<paged::PartHeader *>(base);
+        out->ml = reinterpret_cast<float2 *>(base + hb);
+        out->o = reinterpret_cast<float *>(base + hb + mb);
+        out->row_cap = static_cast<int>(row_cap);
+    }
+    return hb + mb + ob;
+}
+
+constexpr int kRowsKernelMax = 32;                   // rows of its largest item
+
+template <int D, int MT>
+cudaError_t launch_attn_rows(const attn::Maps &maps, const attn::Params &p, int grid, int dev,
+                             cudaStream_t st)
+{
+    constexpr int smem = attn::rows::Cfg<D>::SMEM_BYTES;
+    cudaError_t e = allow_smem<attn::rows::attn_rows_kernel<D, MT>>(dev, smem);
+    if (e == cudaSuccess)
+        e = launch(attn::rows::attn_rows_kernel<D, MT>, dim3(grid), dim3(attn::rows::THREADS),
+                   static_cast<size_t>(smem), st, maps, p);
+    return e;
+}
+
+template <int D>
+int run_attention(attn::Params p, const bitlinear_kv_cache &cache, int64_t max_rows, char *ws,
+                  const DeviceInfo &dev, cudaStream_t st)
+{
+    const int64_t rows = static_cast<int64_t>(p.work.seqs.tokens) * p.work.group;
+    const int grid = std::min(dev.sms, kAttnMaxGrid);
+    p.cache_rows = static_cast<int>(cache.pages * cache.kv_heads * cache.page);
+    p.wait_limit_ns = kWaitLimitNs;
+    attn::Maps maps{};
+    const uint32_t box = static_cast<uint32_t>(std::min<int64_t>(cache.page, attn::rows::BN));
+    if (!make_map_cache(&maps.k, cache.k_dev, cache, box) ||
+        !make_map_cache(&maps.v, cache.v_dev, cache, box))
+        return BITLINEAR_ERR_CUDA;
+    parts_layout(kAttnMaxGrid * attn::rows::WARPS, std::min<int64_t>(rows, kRowsKernelMax), D, ws,
+                 &p.parts);
+    p.work.min_rows = 1;
+    p.work.max_rows = INT_MAX;
+    const bool small = max_rows <= 16;
+    cudaError_t e = small ? launch_attn_rows<D, 1>(maps, p, grid, dev.id, st)
+                          : launch_attn_rows<D, 2>(maps, p, grid, dev.id, st);
+    if (e != cudaSuccess)
+        return launch_status(e);
+    attn::MergeParams mp{p.parts, p.y, p.y_stride, p.lse, p.q_heads, p.work,
+                         grid * attn::rows::WARPS, small ? 16 : 32};
+    e = launch(attn::merge_kernel<D>, dim3(grid * attn::rows::WARPS, small ? 2 : 4),
+               dim3(attn::MERGE_THREADS), 0, st, mp);
+    return launch_status(e);
+}
+
+}  // namespace
+
+extern "C" int bitlinear_rope_append(const void *q_dev, int64_t q_stride, const void *k_dev,
+                                     int64_t k_stride, const void *v_dev, int64_t v_stride,
+                                     int64_t tokens, int64_t q_heads,
+                                     const bitlinear_kv_cache *cache, const bitlinear_seqs *seqs,
+                                     const float *inv_freq_dev, int interleaved,
+                                     const float *q_gain_dev, const float *k_gain_dev,
+                                     float norm_eps, void *q_out_dev, int64_t q_out_stride,
+                                     void *cuda_stream)
+{
+    bool empty = false;
+    int rc = check_paged(tokens, q_heads, cache, seqs, &empty);
+    if (rc != BITLINEAR_OK)
+        return rc;
+    const bool norm = q_gain_dev != nullptr || k_gain_dev != nullptr;
+    if (norm && (!(norm_eps > 0.0f) || !(norm_eps <= FLT_MAX)))
+        return BITLINEAR_ERR_ARG;
+    if (interleaved != 0 && interleaved != 1)
+        return BITLINEAR_ERR_ARG;
+    if (empty)
+        return BITLINEAR_OK;
+    if (inv_freq_dev == nullptr)
+        return BITLINEAR_ERR_ARG;
+    const int64_t D = cache->head_dim;
+    const struct { const void *p; int64_t stride, width; } rows[4] = {
+        {q_dev, q_stride, q_heads * D},
+        {k_dev, k_stride, cache->kv_heads * D},
+        {v_dev, v_stride, cache->kv_heads * D},
+        {q_out_dev, q_out_stride, q_heads * D}};
+    for (const auto &r : rows) {
+        rc = check_rows(r.p, r.stride, r.width);
+        if (rc != BITLINEAR_OK)
+            return rc;
+    }
+    if (!aligned(inv_freq_dev, 4) || !aligned(q_gain_dev, 4) || !aligned(k_gain_dev, 4))
+        return BITLINEAR_ERR_ALIGN;
+    DeviceInfo *dev = nullptr;
+    rc = current_device(&dev);
+    if (rc != BITLINEAR_OK)
+        return rc;
+    rope::Params p{};
+    p.q = static_cast<const uint16_t *>(q_dev);
+    p.k = static_cast<const uint16_t *>(k_dev);
+    p.v = static_cast<const uint16_t *>(v_dev);
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.q_out = static_cast<uint16_t *>(q_out_dev);
+    p.q_out_stride = q_out_stride;
+    p.k_cache = static_cast<uint16_t *>(cache->k_dev);
+    p.v_cache = static_cast<uint16_t *>(cache->v_dev);
+    p.inv_freq = inv_freq_dev;
+    p.q_gain = q_gain_dev;
+    p.k_gain = k_gain_dev;
+    p.eps = norm_eps;
+    p.seqs = device_seqs(*cache, *seqs, tokens);
+    p.q_heads = static_cast<int>(q_heads);
+    p.kv_heads = static_cast<int>(cache->kv_heads);
+    // a row per block until every SM has a few, then several
+    p.per_block = static_cast<int>(
+        std::min<int64_t>(4, std::max<int64_t>(1, tokens / (8 * dev->sms))));
+    const int grid = static_cast<int>((tokens + p.per_block - 1) / p.per_block);
+    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+    return launch_status(D == 64 ? launch_rope<64>(p, interleaved != 0, grid, st)
+                                 : launch_rope<128>(p, interleaved != 0, grid, st));
+}
+
+extern "C" size_t bitlinear_workspace_bytes_attention(int64_t tokens, int64_t seqs,
+                                                      int64_t q_heads, int64_t kv_heads,
+                                                      int64_t head_dim)
+{
+    if (check_paged_shape(tokens, seqs, q_heads, kv_heads, head_dim) != BITLINEAR_OK)
+        return SIZE_MAX;
+    if (tokens == 0 || seqs == 0)
+        return 0;
+    const int64_t rows = tokens * (q_heads / kv_heads);
+    return parts_layout(kAttnMaxGrid * attn::rows::WARPS, std::min<int64_t>(rows, kRowsKernelMax),
+                        head_dim, nullptr, nullptr);
+}
+
+extern "C" int bitlinear_paged_attention(const void *q_dev, int64_t q_stride, int64_t tokens,
+                                         int64_t q_heads, const bitlinear_kv_cache *cache,
+                                         const bitlinear_seqs *seqs, float scale, int64_t window,
+                                         int64_t max_q_len, void *y_dev, int64_t y_stride,
+                                         float *lse_dev_or_null, void *workspace_dev,
+                                         size_t workspace_bytes, void *cuda_stream)
+{
+    bool empty = false;
+    int rc = check_paged(tokens, q_heads, cache, seqs, &empty);
+    if (rc != BITLINEAR_OK)
+        return rc;
+    if (!(scale > 0.0f) || !(scale <= FLT_MAX) || window < 0 || max_q_len < 0)
+        return BITLINEAR_ERR_ARG;
+    if (empty)
+        return BITLINEAR_OK;
+    const int64_t D = cache->head_dim;
+    rc = check_rows(q_dev, q_stride, q_heads * D);
+    if (rc == BITLINEAR_OK)
+        rc = check_rows(y_dev, y_stride, q_heads * D);
+    if (rc != BITLINEAR_OK)
+        return rc;
+    if (!aligned(lse_dev_or_null, 4))
+        return BITLINEAR_ERR_ALIGN;
+    const size_t need = bitlinear_workspace_bytes_attention(tokens, seqs->seqs, q_heads,
+                                                            cache->kv_heads, D);
+    if (workspace_dev == nullptr || workspace_bytes < need)
+        return BITLINEAR_ERR_WORKSPACE;
+    if (!aligned(workspace_dev, 256))
+        return BITLINEAR_ERR_ALIGN;
+    DeviceInfo *dev = nullptr;
+    rc = current_device(&dev);
+    if (rc != BITLINEAR_OK)
+        return rc;
+    attn::Params p{};
+    p.q = static_cast<const uint16_t *>(q_dev);
+    p.y = static_cast<uint16_t *>(y_dev);
+    p.q_stride = q_stride;
+    p.y_stride = y_stride;
+    p.lse = lse_dev_or_null;
+    p.scale_log2 = scale * 1.44269504088896f;
+    p.q_heads = static_cast<int>(q_heads);
+    p.work.seqs = device_seqs(*cache, *seqs, tokens);
+    p.work.kv_heads = static_cast<int>(cache->kv_heads);
+    p.work.group = static_cast<int>(q_heads / cache->kv_heads);
+    p.work.window = static_cast<int>(std::min(window, kAttnMaxKeys));
+    const int64_t longest = max_q_len > 0 ? std::min(max_q_len, tokens) : tokens;
+    cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
+    char *ws = static_cast<char *>(workspace_dev);
+    return D == 64 ? run_attention<64>(p, *cache, longest * p.work.group, ws, *dev, st)
+                   : run_attention<128>(p, *cache, longest * p.work.group, ws, *dev, st);
+}

@@ -1,0 +1,554 @@
+// Attention of few query rows over a paged cache (single tokens, drafted
+// tokens): y_i = sum_j p_ij v_j, p_ij = softmax_j(scale q_i . k_j) over the
+// keys j that row i sees.
+//
+// Every key and value is needed once per key head and each is used by a
+// handful of rows (the query heads of the group times the new tokens), so the
+// kernel is bound by the stream of the cache from HBM. Each warp works on its
+// own: it owns a contiguous run of 32-key slices (paged.cuh), fetches them
+// through its own ring of TMA stages, and computes with mma.sync m16n8k16,
+// whose 16-row tile is the smallest that the tensor pipe offers; the rows of
+// a group fill it, and a warp needs no barrier with any other warp. Tensor
+// maps box the pages with the 128-byte swizzle, so ldmatrix reads keys and
+// (transposed) values without bank conflicts.
+//
+// The softmax runs once over the keys: a row keeps its maximum m, its sum l
+// and its accumulator o in fp32, all relative to m. m is raised only when a
+// score passes it by more than 8 in log2 units: p <= 2^8 stays far inside
+// fp32 and bf16, and the accumulators are rescaled a few times per row instead
+// of once per slice. p is rounded to bf16 for the second product (relative
+// 2^-8 at most, of random sign from key to key, so a row's error stays below
+// the rounding of the output); the sum l takes p before that rounding.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "paged.cuh"
+
+namespace bitlinear {
+namespace attn {
+
+constexpr float RESCALE_AT = 8.0f;     // log2 units
+
+__device__ __forceinline__ float exp2_approx(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi)
+{
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&b);
+}
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int c0, int c1,
+                                            uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
+
+__device__ __forceinline__ void fence_proxy_async()
+{
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+struct Params {
+    const uint16_t *q;         // row t, head h at q + t * q_stride + h * D
+    uint16_t *y;
+    int64_t q_stride, y_stride;
+    float *lse;                // [tokens][q_heads] or null
+    float scale_log2;          // scale * log2(e)
+    int q_heads;
+    int cache_rows;            // pages * kv_heads * page: the first row behind the cache
+    paged::Work work;
+    paged::Parts parts;
+    uint64_t wait_limit_ns;
+};
+
+struct Maps {
+    CUtensorMap k, v;          // {D, cache_rows}, boxes {64, min(page, tile)}, 128-byte swizzle
+};
+
+// Finishes an item's row from its sum and accumulator scale: 1 / l, or 0 for
+// a row that sees no key.
+__device__ __forceinline__ float inv_sum(float l) { return l > 0.0f ? __fdividef(1.0f, l) : 0.0f; }
+
+__device__ __forceinline__ float lse_of(float m, float l)
+{
+    return l > 0.0f ? (m + log2f(l)) * 0.693147180559945f : -INFINITY;
+}
+
+namespace rows {
+
+constexpr int WARPS = 4;
+constexpr int THREADS = WARPS * 32;
+constexpr int BN = 32;                 // keys of a slice
+constexpr int RING_BYTES = 48 * 1024;  // of one warp
+
+template <int D>
+struct Cfg {
+    static constexpr int HALVES = D / 64;
+    static constexpr int HALF_BYTES = BN * 128;
+    static constexpr int TENSOR_BYTES = HALVES * HALF_BYTES;     // the slice's keys (or values)
+    static constexpr int STAGE_BYTES = 2 * TENSOR_BYTES;
+    static constexpr int STAGES = RING_BYTES / STAGE_BYTES;
+    static constexpr int SMEM_BYTES = 1024 + WARPS * RING_BYTES;
+};
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1)
+{
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// MT 16-row tiles per item.
+template <int D, int MT>
+__global__ void __launch_bounds__(THREADS, 1)
+    attn_rows_kernel(const __grid_constant__ Maps maps, const Params p)
+{
+    using C = Cfg<D>;
+    constexpr int BM = 16 * MT;
+    constexpr int KS = D / 16;             // k-steps of the score product
+    constexpr int NT = D / 8;              // 8-channel tiles of the output
+    using Cursor = paged::Cursor<BM, BN>;
+
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ int64_t sums[paged::MAX_GROUPS];
+    __shared__ __align__(8) uint64_t bars[WARPS][C::STAGES];
+    __shared__ int abort_word;
+
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int worker = warp * gridDim.x + blockIdx.x;
+    const int workers = WARPS * gridDim.x;
+    volatile int *abort_flag = &abort_word;
+    const uint32_t ring = ((smem_u32(smem_raw) + 1023u) & ~1023u) + warp * RING_BYTES;
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&maps.k);
+        prefetch_tensormap(&maps.v);
+        abort_word = 0;
+    }
+    if (lane == 0) {
+        for (int i = 0; i < C::STAGES; ++i)
+            mbar_init(smem_u32(&bars[warp][i]), 1);
+        fence_barrier_init();
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    const paged::Work &w = p.work;
+    paged::group_units<BM, BN>(w, warp, WARPS, sums);
+    __syncthreads();
+    int64_t per_head = 0;
+    for (int g = 0; g < (w.seqs.seqs + 31) / 32; ++g)
+        per_head += sums[g];
+    const int64_t units = per_head * w.kv_heads;
+    const int64_t base = units / workers, extra = units % workers;
+    const int64_t u0 = worker * base + min(static_cast<int64_t>(worker), extra);
+    const int64_t count = base + (worker < extra ? 1 : 0);
+
+    paged::PartHeader head[2] = {};
+    if (count > 0) {
+        const int page = 1 << w.seqs.page_shift;
+        const int box = min(page, BN);                 // rows of one TMA box
+        const int subs = BN / box;                     // boxes of a slice and half
+        Cursor ld, cur;
+        cur.seek(w, sums, per_head, u0);
+        ld = cur;
+
+        // Lane i loads the slice's box i: tensor (k, v), half of the channels,
+        // part of the rows. A box without a needed key, or of a page that the
+        // table does not hold, starts behind the cache and is filled with zeros.
+        const int boxes = 2 * C::HALVES * subs;
+        int64_t loaded = 0, done = 0;
+        int ld_stage = 0, stage = 0;
+        uint32_t parity = 0;
+        auto load = [&]() {
+            const int st = ld_stage;
+            ld_stage = ld_stage + 1 == C::STAGES ? 0 : ld_stage + 1;
+            const uint32_t bar = smem_u32(&bars[warp][st]);
+            if (lane == 0)
+                mbar_arrive_expect_tx(bar, C::STAGE_BYTES);
+            __syncwarp();
+            if (lane < boxes) {
+                const int sub = lane % subs;
+                const int half = (lane / subs) % C::HALVES;
+                const bool is_v = lane >= subs * C::HALVES;
+                const int key = ld.tile * BN + sub * box;
+                int row = p.cache_rows;
+                if (key < ld.t.khi && key + box > ld.t.klo) {
+                    const int id = paged::page_of(w.seqs, ld.s, key >> w.seqs.page_shift);
+                    if (id >= 0)
+                        row = ((id * w.kv_heads + ld.h) << w.seqs.page_shift) + (key & (page - 1));
+                }
+                const uint32_t dst = ring + st * C::STAGE_BYTES + (is_v ? C::TENSOR_BYTES : 0) +
+                                     half * C::HALF_BYTES + sub * box * 128;
+                tma_load_2d(dst, is_v ? &maps.v : &maps.k, half * 64, row, bar);
+            }
+            if (++loaded < count && ++ld.tile == ld.t.end)
+                ld.next_item(w);
+        };
+        for (int i = 0; i < C::STAGES && loaded < count; ++i)
+            load();
+
+        bool ok = true;
+        while (ok && done < count) {
+            // ---- one item, or the part of it in this worker's run
+            const bool from_start = cur.tile == cur.t.begin;
+            const int rows = min(BM, cur.v.qlen * w.group - cur.m * BM);
+            const int pos0 = cur.v.kv - cur.v.qlen;
+            const int r_lo = lane >> 2;                // rows r_lo and r_lo + 8 of each 16-row tile
+            uint32_t qf[MT][KS][4];
+            int seen_hi[2 * MT];                       // last key the row sees
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = mt * 16 + e * 8 + r_lo;
+                    const int rr = cur.m * BM + r;
+                    const int tok = rr / w.group;
+                    seen_hi[2 * mt + e] = pos0 + tok;
+                    const uint32_t *src = reinterpret_cast<const uint32_t *>(
+                        p.q + (cur.v.q0 + tok) * p.q_stride +
+                        (cur.h * w.group + rr - tok * w.group) * D + (lane & 3) * 2);
+#pragma unroll
+                    for (int ks = 0; ks < KS; ++ks) {
+                        qf[mt][ks][e] = r < rows ? __ldg(src + ks * 8) : 0u;
+                        qf[mt][ks][2 + e] = r < rows ? __ldg(src + ks * 8 + 4) : 0u;
+                    }
+                }
+            }
+            float o[MT][NT][4];
+            float m[2 * MT], l[2 * MT];
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i) {
+                m[i] = -INFINITY;
+                l[i] = 0.0f;
+            }
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        o[mt][n][i] = 0.0f;
+
+            // keys every row of the item sees: slices inside need no mask
+            const int all_hi = pos0 + (cur.m * BM) / w.group;
+            const int all_lo = w.window > 0 ? cur.t.khi - w.window : 0;
+            for (; done < count; ) {
+                const uint32_t bar = smem_u32(&bars[warp][stage]);
+                if (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)) &&
+                    !warp_wait_bounded(bar, parity, abort_flag, p.wait_limit_ns)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t ks_base = ring + stage * C::STAGE_BYTES;
+                const uint32_t vs_base = ks_base + C::TENSOR_BYTES;
+                const int key0 = cur.tile * BN;
+                if (key0 < cur.t.klo || key0 + BN > cur.t.khi) {
+                    // slots that hold no key of the sequence may hold anything,
+                    // and 0 * NaN is NaN: their values become zeros
+                    const int key = key0 + lane;
+                    if (key < cur.t.klo || key >= cur.t.khi) {
+#pragma unroll
+                        for (int i = 0; i < C::HALVES * 8; ++i)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                             vs_base + (i >> 3) * C::HALF_BYTES + lane * 128 +
+                                             (i & 7) * 16),
+                                         "r"(0)
+                                         : "memory");
+                    }
+                    fence_proxy_async();
+                    __syncwarp();
+                }
+
+                // ---- scores of 16 MT rows and 32 keys
+                float s[MT][4][4];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            s[mt][n][i] = 0.0f;
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+                    for (int np = 0; np < 2; ++np) {   // two 8-key tiles at a time
+                        const int row = np * 16 + (lane & 7) + ((lane & 16) >> 1);
+                        const int chunk = (ks & 3) * 2 + ((lane >> 3) & 1);
+                        uint32_t b[4];
+                        ldsm4(b, ks_base + (ks >> 2) * C::HALF_BYTES + row * 128 +
+                                     ((chunk ^ (row & 7)) << 4));
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            mma_bf16(s[mt][2 * np], qf[mt][ks], b[0], b[1]);
+                            mma_bf16(s[mt][2 * np + 1], qf[mt][ks], b[2], b[3]);
+                        }
+                    }
+                }
+                if (key0 + BN - 1 > all_hi || key0 < all_lo) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int n = 0; n < 4; ++n)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int key = key0 + n * 8 + (lane & 3) * 2 + (i & 1);
+                                const int hi = seen_hi[2 * mt + (i >> 1)];
+                                if (key > hi || (w.window > 0 && key <= hi - w.window))
+                                    s[mt][n][i] = -INFINITY;
+                            }
+                }
+
+                // ---- running maximum and sum
+                float sub[2 * MT];
+#pragma unroll
+                for (int i = 0; i < 2 * MT; ++i) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+                        top = fmaxf(top, fmaxf(s[i >> 1][n][2 * (i & 1)],
+                                               s[i >> 1][n][2 * (i & 1) + 1]));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    top *= p.scale_log2;
+                    const bool raise = top > m[i] + RESCALE_AT;     // also from -inf
+                    if (__any_sync(0xffffffffu, raise)) {
+                        if (raise) {
+                            const float f = exp2_approx(m[i] - top);
+                            m[i] = top;
+                            l[i] *= f;
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                o[i >> 1][n][2 * (i & 1)] *= f;
+                                o[i >> 1][n][2 * (i & 1) + 1] *= f;
+                            }
+                        }
+                    }
+                    sub[i] = m[i] == -INFINITY ? 0.0f : m[i];
+                }
+                uint32_t pf[MT][2][4];                 // p as the second product's A operand
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        float e[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            e[i] = exp2_approx(
+                                fmaf(s[mt][n][i], p.scale_log2, -sub[2 * mt + (i >> 1)]));
+                        l[2 * mt] += e[0] + e[1];
+                        l[2 * mt + 1] += e[2] + e[3];
+                        pf[mt][n >> 1][(n & 1) * 2] = pack_bf16(e[0], e[1]);
+                        pf[mt][n >> 1][(n & 1) * 2 + 1] = pack_bf16(e[2], e[3]);
+                    }
+
+                // ---- o += p v
+#pragma unroll
+                for (int kk = 0; kk < 2; ++kk) {       // 16 keys at a time
+                    const int row = kk * 16 + (lane & 15);
+#pragma unroll
+                    for (int np = 0; np < NT / 2; ++np) {
+                        const int chunk = (np & 3) * 2 + (lane >> 4);
+                        uint32_t b[4];
+                        ldsm4_t(b, vs_base + (np >> 2) * C::HALF_BYTES + row * 128 +
+                                       ((chunk ^ (row & 7)) << 4));
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            mma_bf16(o[mt][2 * np], pf[mt][kk], b[0], b[1]);
+                            mma_bf16(o[mt][2 * np + 1], pf[mt][kk], b[2], b[3]);
+                        }
+                    }
+                }
+                __syncwarp();                          // every lane has read the stage
+                ++done;
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    parity ^= 1u;
+                }
+                if (loaded < count)
+                    load();
+                if (++cur.tile == cur.t.end)
+                    break;
+            }
+            if (!ok)
+                break;
+
+            // ---- the item's rows, or their part
+            const bool to_end = cur.tile == cur.t.end;
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i) {
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+            }
+            const int slot = 2 * worker + (from_start ? 1 : 0);
+            const bool whole = from_start && to_end;
+#pragma unroll
+            for (int i = 0; i < 2 * MT; ++i) {
+                const int r = (i >> 1) * 16 + (i & 1) * 8 + r_lo;
+                if (r >= rows)
+                    continue;
+                if (whole) {
+                    const int rr = cur.m * BM + r;
+                    const int tok = rr / w.group;
+                    const int hq = cur.h * w.group + rr - tok * w.group;
+                    const float f = inv_sum(l[i]);
+                    uint32_t *dst = reinterpret_cast<uint32_t *>(
+                        p.y + (cur.v.q0 + tok) * p.y_stride + hq * D + (lane & 3) * 2);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        dst[n * 4] = pack_bf16(o[i >> 1][n][2 * (i & 1)] * f,
+                                               o[i >> 1][n][2 * (i & 1) + 1] * f);
+                    if (p.lse != nullptr && (lane & 3) == 0)
+                        p.lse[static_cast<int64_t>(cur.v.q0 + tok) * p.q_heads + hq] =
+                            lse_of(m[i], l[i]);
+                } else {
+                    const int64_t at = static_cast<int64_t>(slot) * p.parts.row_cap + r;
+                    float2 *dst = reinterpret_cast<float2 *>(p.parts.o + at * D) + (lane & 3);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        dst[n * 4] = make_float2(o[i >> 1][n][2 * (i & 1)],
+                                                 o[i >> 1][n][2 * (i & 1) + 1]);
+                    if ((lane & 3) == 0)
+                        p.parts.ml[at] = make_float2(m[i], l[i]);
+                }
+            }
+            if (!whole)
+                head[from_start ? 1 : 0] =
+                    paged::PartHeader{to_end ? 2 : 1, cur.s, cur.m, cur.h};
+            if (done < count)
+                cur.next_item(w);
+        }
+        if (!ok) {
+            // leave no copy in flight behind, and no part that could be merged
+            for (; lane == 0 && done < loaded; ++done) {
+                drain_wait(smem_u32(&bars[warp][stage]), parity, p.wait_limit_ns);
+                if (++stage == C::STAGES) {
+                    stage = 0;
+                    parity ^= 1u;
+                }
+            }
+            head[0].state = head[1].state = 0;
+        }
+    }
+    if (lane < 2)
+        p.parts.headers[2 * worker + lane] = lane == 0 ? head[0] : head[1];
+}
+
+}  // namespace rows
+
+// ------------------------------------------------------------------- merge
+//
+// Joins the parts of the items that were split between workers, in the order
+// of their keys: o = sum_i 2^(m_i - M) o_i and l likewise, M the largest m_i.
+// Block (x, y) looks at worker x's second slot, where a split item begins, and
+// takes every gridDim.y-th row block of it.
+
+constexpr int MERGE_THREADS = 128;
+
+struct MergeParams {
+    paged::Parts parts;
+    uint16_t *y;
+    int64_t y_stride;
+    float *lse;
+    int q_heads;
+    paged::Work work;
+    int workers;
+    int item_rows;             // BM of the kernel that left the parts
+};
+
+template <int D>
+__global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const MergeParams p)
+{
+    constexpr int TPR = D / 4;                         // threads per row
+    constexpr int ROWS = MERGE_THREADS / TPR;
+    pdl_wait();
+    pdl_launch_dependents();
+    const int first = 2 * blockIdx.x + 1;
+    const paged::PartHeader hd = p.parts.headers[first];
+    if (hd.state != 1)
+        return;
+    // the item goes on in the first slots of the following workers; every warp
+    // looks at 32 of them at a time for the last part
+    int parts = 1;
+    for (int wk = blockIdx.x + 1;; wk += 32) {
+        const int mine = wk + (threadIdx.x & 31);
+        const int state = mine < p.workers ? p.parts.headers[2 * mine].state : 0;
+        const unsigned ends = __ballot_sync(0xffffffffu, state != 1);
+        if (ends == 0) {
+            parts += 32;
+            continue;
+        }
+        const int at = __ffs(ends) - 1;
+        if (__shfl_sync(0xffffffffu, state, at) != 2)
+            return;                                    // a worker gave up: nothing to join
+        parts += at + 1;
+        break;
+    }
+    const paged::View v = paged::view(p.work.seqs, hd.s);
+    const int group = p.work.group;
+    const int rows = min(p.item_rows, v.qlen * group - hd.m * p.item_rows);
+    const int c = threadIdx.x % TPR;
+    for (int r = blockIdx.y * ROWS + threadIdx.x / TPR; r < rows; r += gridDim.y * ROWS) {
+        auto at = [&](int i) {
+            const int slot = i == 0 ? first : first + 2 * i - 1;
+            return static_cast<int64_t>(slot) * p.parts.row_cap + r;
+        };
+        float top = -INFINITY;
+#pragma unroll 8
+        for (int i = 0; i < parts; ++i)
+            top = fmaxf(top, p.parts.ml[at(i)].x);
+        const float sub = top == -INFINITY ? 0.0f : top;
+        float l = 0.0f;
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+        for (int i = 0; i < parts; ++i) {
+            const float2 ml = p.parts.ml[at(i)];
+            const float4 x = *reinterpret_cast<const float4 *>(p.parts.o + at(i) * D + 4 * c);
+            const float f = exp2_approx(ml.x - sub);
+            l = fmaf(ml.y, f, l);
+            o.x = fmaf(x.x, f, o.x);
+            o.y = fmaf(x.y, f, o.y);
+            o.z = fmaf(x.z, f, o.z);
+            o.w = fmaf(x.w, f, o.w);
+        }
+        const int rr = hd.m * p.item_rows + r;
+        const int tok = rr / group;
+        const int hq = hd.h * group + rr - tok * group;
+        const float f = inv_sum(l);
+        *reinterpret_cast<uint2 *>(p.y + (v.q0 + tok) * p.y_stride + hq * D + 4 * c) =
+            make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
+        if (p.lse != nullptr && c == 0)
+            p.lse[static_cast<int64_t>(v.q0 + tok) * p.q_heads + hq] = lse_of(top, l);
+    }
+}
+
+}  // namespace attn
+}  // namespace bitlinear

@@ -24,6 +24,9 @@
 #include "quant_act.cuh"
 #include "stage_io.cuh"
 #include "ffn_act.cuh"
+#include "paged.cuh"
+#include "rope_append.cuh"
+#include "attn_rows.cuh"
 
 using namespace bitlinear;
 
@@ -931,6 +934,7 @@ extern "C" const char *bitlinear_status_string(int status)
     case BITLINEAR_ERR_HOST: return "host allocation failed";
     case BITLINEAR_ERR_IO: return "file could not be read or written";
     case BITLINEAR_ERR_FORMAT: return "not a valid packed-weight file";
+    case BITLINEAR_ERR_INDEX: return "index in device memory out of range";
     default: return "unknown status";
     }
 }
@@ -1557,7 +1561,7 @@ extern "C" int bitlinear_get_fault(int *fault_out, void *cuda_stream)
         const unsigned int zero = 0;
         if (cudaMemcpyToSymbol(g_fault_word, &zero, sizeof(zero)) != cudaSuccess)
             return BITLINEAR_ERR_CUDA;
-        return BITLINEAR_ERR_TIMEOUT;
+        return (word & FAULT_WAIT_TIMEOUT) != 0 ? BITLINEAR_ERR_TIMEOUT : BITLINEAR_ERR_INDEX;
     }
     return BITLINEAR_OK;
 }
@@ -1620,3 +1624,7 @@ extern "C" int bitlinear_forward_noalloc(const void *x_dev, bitlinear_dtype xdt,
                        nullptr, nullptr, nullptr, *dev, static_cast<cudaStream_t>(cuda_stream),
                        0, false);
 }
+
+// ================================================= attention on a paged cache
+
+#include "attn_host.cuh"

@@ -16,6 +16,7 @@ __device__ unsigned int g_fault_word;
 enum FaultCode : unsigned int {
     FAULT_NONE = 0,
     FAULT_WAIT_TIMEOUT = 1,
+    FAULT_BAD_INDEX = 2,        // a sequence, length or page index in device memory out of range
 };
 
 // ------------------------------------------------------------------ basics

@@ -1,0 +1,166 @@
+"""The paged-cache operators refuse bad arguments on the host: every check here
+returns before the library touches CUDA."""
+import ctypes
+
+import pytest
+import torch
+
+import ternary_weight_w1_b200 as bl
+
+FAKE = 1 << 20          # a 256-byte-aligned non-null address; never dereferenced
+BIG = 1 << 40
+
+
+def descriptors(kw):
+    c = dict(k=FAKE, v=FAKE, pages=10, kv_heads=2, page=16, head_dim=64)
+    s = dict(q_start=FAKE, kv_len=FAKE, table=FAKE, seqs=1, cols=4)
+    for d in (c, s):
+        d.update({n: kw.pop(n) for n in list(kw) if n in d})
+    return (bl._KVCache(c["k"], c["v"], c["pages"], c["kv_heads"], c["page"], c["head_dim"]),
+            bl._Seqs(s["q_start"], s["kv_len"], s["table"], s["seqs"], s["cols"]))
+
+
+def append(**kw):
+    cache, seqs = descriptors(kw)
+    a = dict(q=FAKE, qs=256, kk=FAKE, ks=128, vv=FAKE, vs=128, T=3, heads=4,
+             cache=ctypes.addressof(cache), sq=ctypes.addressof(seqs), f=FAKE, inter=0, qg=None,
+             kg=None, eps=1e-6, out=FAKE, os=256, stream=None)
+    a.update(kw)
+    return bl.lib().bitlinear_rope_append(*a.values())
+
+
+def attend(**kw):
+    cache, seqs = descriptors(kw)
+    a = dict(q=FAKE, qs=256, T=3, heads=4, cache=ctypes.addressof(cache),
+             sq=ctypes.addressof(seqs), scale=0.125, window=0, max_q=0, y=FAKE, ys=256, lse=None,
+             ws=FAKE, wsb=BIG, stream=None)
+    a.update(kw)
+    return bl.lib().bitlinear_paged_attention(*a.values())
+
+
+SHARED = [
+    (dict(cache=None), bl.BITLINEAR_ERR_ARG),
+    (dict(sq=None), bl.BITLINEAR_ERR_ARG),
+    (dict(k=None), bl.BITLINEAR_ERR_ARG),
+    (dict(v=None), bl.BITLINEAR_ERR_ARG),
+    (dict(q_start=None), bl.BITLINEAR_ERR_ARG),
+    (dict(kv_len=None), bl.BITLINEAR_ERR_ARG),
+    (dict(table=None), bl.BITLINEAR_ERR_ARG),
+    (dict(q=None), bl.BITLINEAR_ERR_ARG),
+    (dict(T=-1), bl.BITLINEAR_ERR_ARG),
+    (dict(heads=0), bl.BITLINEAR_ERR_ARG),
+    (dict(kv_heads=0), bl.BITLINEAR_ERR_ARG),
+    (dict(pages=0), bl.BITLINEAR_ERR_ARG),
+    (dict(cols=0), bl.BITLINEAR_ERR_ARG),
+    (dict(seqs=-1), bl.BITLINEAR_ERR_ARG),
+    (dict(heads=3), bl.BITLINEAR_ERR_SHAPE),              # not a multiple of the key heads
+    (dict(heads=65538, qs=65538 * 64), bl.BITLINEAR_ERR_SHAPE),
+    (dict(head_dim=96), bl.BITLINEAR_ERR_SHAPE),
+    (dict(head_dim=256), bl.BITLINEAR_ERR_SHAPE),
+    (dict(head_dim=0), bl.BITLINEAR_ERR_SHAPE),
+    (dict(page=8), bl.BITLINEAR_ERR_SHAPE),
+    (dict(page=24), bl.BITLINEAR_ERR_SHAPE),
+    (dict(page=512), bl.BITLINEAR_ERR_SHAPE),
+    (dict(page=-16), bl.BITLINEAR_ERR_SHAPE),
+    (dict(page=0), bl.BITLINEAR_ERR_SHAPE),
+    (dict(seqs=16385), bl.BITLINEAR_ERR_SHAPE),
+    (dict(T=1 << 29), bl.BITLINEAR_ERR_SHAPE),
+    (dict(T=1 << 62), bl.BITLINEAR_ERR_SHAPE),
+    (dict(cols=1 << 27), bl.BITLINEAR_ERR_SHAPE),
+    (dict(pages=1 << 27), bl.BITLINEAR_ERR_SHAPE),
+    (dict(pages=1 << 62), bl.BITLINEAR_ERR_SHAPE),
+    (dict(kv_heads=1 << 40, heads=1 << 40), bl.BITLINEAR_ERR_SHAPE),
+    (dict(qs=255), bl.BITLINEAR_ERR_SHAPE),               # rows would overlap
+    (dict(qs=260), bl.BITLINEAR_ERR_ALIGN),
+    (dict(q=FAKE + 8), bl.BITLINEAR_ERR_ALIGN),
+    (dict(k=FAKE + 8), bl.BITLINEAR_ERR_ALIGN),
+    (dict(v=FAKE + 2), bl.BITLINEAR_ERR_ALIGN),
+    (dict(q_start=FAKE + 2), bl.BITLINEAR_ERR_ALIGN),
+    (dict(kv_len=FAKE + 1), bl.BITLINEAR_ERR_ALIGN),
+    (dict(table=FAKE + 2), bl.BITLINEAR_ERR_ALIGN),
+    # no token or no sequence: nothing to do, no pointer is needed
+    (dict(T=0), bl.BITLINEAR_OK),
+    (dict(seqs=0), bl.BITLINEAR_OK),
+    (dict(T=0, q=None, k=None, v=None, q_start=None, kv_len=None, table=None), bl.BITLINEAR_OK),
+]
+
+
+@pytest.mark.parametrize("call", [append, attend])
+@pytest.mark.parametrize("kw,status", SHARED)
+def test_shared_refusals(call, kw, status):
+    assert call(**dict(kw)) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(kk=None), bl.BITLINEAR_ERR_ARG),
+    (dict(vv=None), bl.BITLINEAR_ERR_ARG),
+    (dict(f=None), bl.BITLINEAR_ERR_ARG),
+    (dict(out=None), bl.BITLINEAR_ERR_ARG),
+    (dict(inter=2), bl.BITLINEAR_ERR_ARG),
+    (dict(qg=FAKE, eps=0.0), bl.BITLINEAR_ERR_ARG),
+    (dict(kg=FAKE, eps=float("nan")), bl.BITLINEAR_ERR_ARG),
+    (dict(kg=FAKE, eps=float("inf")), bl.BITLINEAR_ERR_ARG),
+    (dict(ks=64), bl.BITLINEAR_ERR_SHAPE),
+    (dict(vs=-128), bl.BITLINEAR_ERR_SHAPE),
+    (dict(vs=132), bl.BITLINEAR_ERR_ALIGN),
+    (dict(kk=FAKE + 4), bl.BITLINEAR_ERR_ALIGN),
+    (dict(out=FAKE + 2), bl.BITLINEAR_ERR_ALIGN),
+    (dict(f=FAKE + 2), bl.BITLINEAR_ERR_ALIGN),
+    (dict(qg=FAKE + 1), bl.BITLINEAR_ERR_ALIGN),
+    (dict(kg=FAKE + 2), bl.BITLINEAR_ERR_ALIGN),
+])
+def test_append_refusals(kw, status):
+    assert append(**kw) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(y=None), bl.BITLINEAR_ERR_ARG),
+    (dict(scale=0.0), bl.BITLINEAR_ERR_ARG),
+    (dict(scale=-1.0), bl.BITLINEAR_ERR_ARG),
+    (dict(scale=float("nan")), bl.BITLINEAR_ERR_ARG),
+    (dict(scale=float("inf")), bl.BITLINEAR_ERR_ARG),
+    (dict(window=-1), bl.BITLINEAR_ERR_ARG),
+    (dict(max_q=-1), bl.BITLINEAR_ERR_ARG),
+    (dict(ys=128), bl.BITLINEAR_ERR_SHAPE),
+    (dict(ys=257), bl.BITLINEAR_ERR_ALIGN),
+    (dict(y=FAKE + 8), bl.BITLINEAR_ERR_ALIGN),
+    (dict(lse=FAKE + 2), bl.BITLINEAR_ERR_ALIGN),
+    (dict(ws=None), bl.BITLINEAR_ERR_WORKSPACE),
+    (dict(wsb=64), bl.BITLINEAR_ERR_WORKSPACE),
+    (dict(ws=FAKE + 128), bl.BITLINEAR_ERR_ALIGN),
+])
+def test_attention_refusals(kw, status):
+    assert attend(**kw) == status
+
+
+def test_attention_workspace_bytes():
+    size_max = ctypes.c_size_t(-1).value
+    ws = bl.bitlinear_workspace_bytes_attention
+    assert 0 < ws(1, 1, 20, 5, 128) < 16 << 20
+    assert ws(1, 1, 20, 5, 128) <= ws(100, 1, 20, 5, 128) <= ws(5000, 1, 20, 5, 128) < 256 << 20
+    assert ws(0, 1, 20, 5, 128) == 0 and ws(1, 0, 20, 5, 128) == 0
+    for bad in ((-1, 1, 20, 5, 128), (1, 1, 20, 3, 128), (1, 1, 20, 5, 80), (1, 16385, 20, 5, 128),
+                (1 << 40, 1, 20, 5, 128)):
+        assert ws(*bad) == size_max
+
+
+def host_step():
+    c = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    i = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    return dict(q=torch.zeros(3, 4, 64, dtype=torch.bfloat16), k_cache=c, v_cache=c.clone(),
+                q_start=i(2), kv_len=i(1), page_table=i(1, 4))
+
+
+def test_binding_refuses_host_tensors_and_wrong_shapes():
+    kv = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    for call in (lambda a: bl.bitlinear_paged_attention(**a),
+                 lambda a: bl.bitlinear_rope_append(k=kv, v=kv, inv_freq=torch.zeros(32), **a)):
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            call(host_step())
+        with pytest.raises(ValueError, match="pages"):
+            call(dict(host_step(), k_cache=torch.zeros(4, 64)))
+        with pytest.raises(ValueError, match="page_table"):
+            call(dict(host_step(), page_table=torch.zeros(4, dtype=torch.int32)))
+        with pytest.raises(bl.BitLinearError) as e:
+            call(dict(host_step(), k_cache=torch.zeros(4, 2, 16, 80, dtype=torch.bfloat16)))
+        assert e.value.status == bl.BITLINEAR_ERR_SHAPE

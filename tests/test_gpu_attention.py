@@ -1,0 +1,269 @@
+"""Attention over the paged cache (bitlinear_paged_attention) against a plain
+64-bit form, at the shapes, masks and index patterns where it can go wrong."""
+import math
+
+import pytest
+import torch
+
+import ternary_weight_w1_b200 as bl
+from tests.paged_cases import Step
+
+pytestmark = pytest.mark.gpu
+
+CANARY = 0.4375
+
+
+@pytest.fixture(scope="module", autouse=True)
+def cuda():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    bl.lib()
+    yield
+    assert bl.bitlinear_get_fault() == (bl.BITLINEAR_OK, 0)
+
+
+def check(step, window=0, scale=None, max_q_len=None):
+    y = torch.full((step.rows, step.hq, step.d), CANARY, dtype=torch.bfloat16, device="cuda")
+    lse = torch.zeros((step.rows, step.hq), device="cuda")
+    need = bl.bitlinear_workspace_bytes_attention(step.rows, len(step.lens), step.hq, step.hkv,
+                                                  step.d)
+    ws = torch.full((need,), 0xFF, dtype=torch.uint8, device="cuda")   # no initialisation needed
+    out = step.attend(y=y, lse=lse, workspace=ws, window=window, scale=scale, max_q_len=max_q_len)
+    assert out is y
+    step.check_attention(y, lse, CANARY, scale, window)
+    return y, lse
+
+
+# heads: groups of 1, 2, 3, 4, 5, 8, 12, 16 and 20 query heads per key head
+HEADS = [(4, 4, 64), (4, 2, 64), (6, 2, 128), (20, 5, 128), (5, 1, 64), (8, 1, 128), (24, 2, 128),
+         (16, 1, 64), (20, 1, 128)]
+
+
+@pytest.mark.parametrize("heads", HEADS)
+@pytest.mark.parametrize("page", [16, 64])
+def test_single_tokens(heads, page):
+    check(Step([(1, 1), (1, 700), (1, 31), (1, 32), (1, 33), (1, 129)], heads, page, seed=1),
+          max_q_len=1)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("d", [64, 128])
+def test_page_sizes(page, d):
+    lens = [(1, page - 1), (1, page), (1, page + 1), (3, 3 * page + 5), (40, 2 * page + 7)]
+    check(Step(lens, (8, 2, d), page, seed=2))
+
+
+@pytest.mark.parametrize("heads", HEADS)
+def test_drafts(heads):
+    check(Step([(5, 5), (2, 300), (4, 63), (5, 1000)], heads, 32, seed=3), max_q_len=5)
+
+
+@pytest.mark.parametrize("q,kv", [(1, 4099), (2, 2), (7, 7), (16, 16), (33, 33), (64, 200),
+                                  (127, 127), (128, 128), (129, 129), (255, 300), (300, 1000),
+                                  (513, 513)])
+@pytest.mark.parametrize("heads", [(8, 2, 64), (20, 5, 128), (3, 3, 128), (6, 1, 64)])
+def test_chunk_lengths(q, kv, heads):
+    check(Step([(q, kv)], heads, 64, seed=q + kv))
+
+
+@pytest.mark.parametrize("heads", [(8, 2, 64), (20, 5, 128)])
+@pytest.mark.parametrize("page", [16, 128])
+def test_mixed_batch(heads, page):
+    lens = [(1, 77), (200, 333), (1, 1), (0, 50), (1, 1500), (90, 90), (0, 0), (5, 2000)]
+    step = Step(lens, heads, page, seed=5, spare=9, front=3)
+    check(step)
+    check(step, max_q_len=200)
+
+
+@pytest.mark.parametrize("window", [1, 2, 16, 31, 64, 100, 129, 5000])
+@pytest.mark.parametrize("heads", [(8, 2, 64), (20, 5, 128)])
+def test_window(window, heads):
+    check(Step([(1, 900), (40, 300), (1, 20), (150, 150), (3, 65)], heads, 16, seed=6),
+          window=window)
+
+
+def test_pages_in_front_of_the_window_are_not_needed():
+    # a server frees them: their table entries are gone, their slots rewritten
+    step = Step([(1, 900), (40, 700), (300, 900)], (8, 2, 64), 16, seed=7)
+    window, want = 100, None
+    want = step.attention(window=window)
+    for s, at, n, kv in step.spans():
+        gone = max(0, kv - n - window + 1) // 16
+        step.k_cache[step.table[s, :gone].long()] = math.nan
+        step.v_cache[step.table[s, :gone].long()] = math.nan
+        step.table[s, :gone] = -1
+    y = step.attend(window=window)
+    off = (y.double() - want[0]).abs()
+    assert (off <= want[1]).all()
+
+
+def test_rows_that_see_nothing():
+    # more rows than the cache holds: the first ones stand before position 0
+    step = Step([(10, 4), (3, 0), (50, 20), (1, 0), (300, 130)], (8, 2, 64), 16, seed=8)
+    y, lse = check(step)
+    none = torch.isinf(lse[:, 0])
+    assert none.sum() == 6 + 3 + 30 + 1 + 170 and (y[none] == 0).all()
+
+
+@pytest.mark.parametrize("lens", [[], [(0, 0)], [(0, 5), (0, 0)]])
+def test_nothing_to_do(lens):
+    step = Step(lens, spare=2)
+    y = torch.full((2, 4, 64), CANARY, dtype=torch.bfloat16, device="cuda")
+    step.attend(y=y)
+    assert (y == CANARY).all()
+
+
+@pytest.mark.parametrize("scale", [1e-3, 0.5, 4.0])
+def test_scale(scale):
+    # at the largest a row's weight sits on one key, far above the others
+    check(Step([(1, 500), (70, 400)], (8, 2, 64), 32, seed=9), scale=scale)
+
+
+@pytest.mark.parametrize("rising", [True, False])
+@pytest.mark.parametrize("q", [1, 80])
+def test_scores_that_grow_and_fall_along_the_keys(rising, q):
+    # every tile of keys raises the running maximum, or none after the first
+    step = Step([(q, 1500)], (4, 1, 64), 64, seed=10)
+    ramp = torch.linspace(0.05, 4.0, 1500)
+    ramp = (ramp if rising else ramp.flip(0)).cuda()
+    direction = torch.randn(64, generator=torch.Generator().manual_seed(3)).cuda()
+    at = step.table[0].long()[:-(-1500 // 64)]
+    k = (ramp[:, None] * direction).to(torch.bfloat16)
+    full = torch.full((len(at) * 64, 64), math.nan, dtype=torch.bfloat16, device="cuda")
+    full[:1500] = k
+    step.k_cache[at, 0] = full.view(len(at), 64, 64)
+    step.q[:] = direction.to(torch.bfloat16)
+    check(step, scale=1.0)
+
+
+def test_large_and_small_values():
+    step = Step([(1, 300), (60, 260)], (4, 2, 128), 16, seed=11)
+    step.v_cache.mul_(1e30)
+    check(step)
+    step.v_cache.mul_(1e-38)
+    step.q.mul_(1e-20)
+    check(step)
+
+
+def test_many_sequences():
+    gen = torch.Generator().manual_seed(4)
+    lens = [(int(n > 2), int(kv)) for n, kv in zip(torch.randint(0, 12, (1100,), generator=gen),
+                                                   torch.randint(1, 90, (1100,), generator=gen))]
+    check(Step(lens, (4, 1, 64), 16, seed=12), max_q_len=1)
+
+
+def test_one_long_sequence_among_short_ones():
+    check(Step([(1, 5), (1, 40000), (1, 3), (1, 64)], (8, 2, 128), 128, seed=13), max_q_len=1)
+
+
+def test_shared_prefix_pages():
+    step = Step([(1, 130), (6, 140), (30, 150)], (4, 2, 64), 16, seed=14)
+    step.table[1:, :8] = step.table[0, :8]         # 128 positions in common
+    check(step)
+
+
+def test_strided_queries_and_outputs():
+    # queries as the front part of a fused projection's rows, outputs into a
+    # wider buffer, two-dimensional rows
+    step = Step([(1, 77), (40, 90), (3, 3)], (4, 2, 64), 16, seed=15)
+    wide = torch.full((step.rows, 640), math.nan, dtype=torch.bfloat16, device="cuda")
+    wide[:, 64:320] = step.q.flatten(1)
+    out = torch.full((step.rows, 512), CANARY, dtype=torch.bfloat16, device="cuda")
+    y = step.attend(q=wide[:, 64:320], y=out[:, 128:384])
+    step.check_attention(y)
+    assert (out[:, :128] == CANARY).all() and (out[:, 384:] == CANARY).all()
+    assert torch.equal(step.attend(q=wide[:, 64:320].view(step.rows, 4, 64)).flatten(1), y)
+
+
+def test_a_hint_that_is_too_small_only_costs_time():
+    step = Step([(1, 50), (130, 200), (20, 20)], (8, 2, 64), 16, seed=16)
+    check(step, max_q_len=1)
+
+
+def test_same_bits_every_time():
+    step = Step([(1, 3000), (200, 700), (1, 64), (12, 900)], (20, 5, 128), 64, seed=17)
+    first = step.attend()
+    for _ in range(3):
+        assert torch.equal(step.attend().view(torch.int16), first.view(torch.int16))
+
+
+def test_captured_step_follows_the_lengths_on_the_device():
+    # one graph, captured for the largest step, replayed while tokens arrive
+    step = Step([(2, 40), (60, 400), (1, 200)], (8, 2, 64), 16, seed=18)
+    y = torch.zeros((step.rows, 8, 64), dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(bl.bitlinear_workspace_bytes_attention(step.rows, 3, 8, 2, 64),
+                     dtype=torch.uint8, device="cuda")
+    step.attend(y=y, workspace=ws)                     # outside the capture first
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step.attend(y=y, workspace=ws)
+    for lens in ([(2, 40), (60, 400), (1, 200)], [(1, 33), (60, 60), (0, 0)],
+                 [(0, 40), (1, 399), (1, 17)], [(0, 0), (0, 0), (63, 180)]):
+        start = torch.tensor([0] + [n for n, _ in lens]).cumsum(0)
+        step.q_start.copy_(start.to(torch.int32))
+        step.kv_len.copy_(torch.tensor([kv for _, kv in lens], dtype=torch.int32))
+        step.lens = lens
+        step.live = torch.arange(step.rows, device="cuda") < int(start[-1])
+        y.fill_(CANARY)
+        graph.replay()
+        step.check_attention(y, canary=CANARY)
+
+
+def test_two_graphs_share_a_workspace_one_after_the_other():
+    a = Step([(1, 5000)], (8, 2, 128), 64, seed=19)
+    b = Step([(100, 300), (1, 4000)], (20, 5, 128), 32, seed=20)
+    need = max(bl.bitlinear_workspace_bytes_attention(s.rows, len(s.lens), s.hq, s.hkv, s.d)
+               for s in (a, b))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    outs, graphs = [], []
+    for s in (a, b):
+        y = torch.zeros((s.rows, s.hq, s.d), dtype=torch.bfloat16, device="cuda")
+        s.attend(y=y, workspace=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            s.attend(y=y, workspace=ws)
+        outs.append(y)
+        graphs.append(g)
+    for i in (0, 1, 1, 0, 1, 0):
+        outs[i].zero_()
+        graphs[i].replay()
+        (a, b)[i].check_attention(outs[i])
+
+
+def test_streams():
+    # two steps on two streams at once, each with what the call allocates
+    steps = [Step([(1, 3000), (64, 500)], (8, 2, 64), 16, seed=21),
+             Step([(1, 2500), (1, 100)], (20, 5, 128), 64, seed=22)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[], []]
+    for _ in range(6):
+        for i in (0, 1):
+            outs[i].append(steps[i].attend(stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        steps[i].check_attention(outs[i][0])
+        assert all(torch.equal(o.view(torch.int16), outs[i][0].view(torch.int16)) for o in outs[i])
+
+
+@pytest.mark.parametrize("q", [1, 100])
+def test_bad_indexes_are_reported_and_not_used(q):
+    # CPU reading first: every index passes view() or page_of() before an access
+    good = Step([(q, 150), (q, 90)], (8, 2, 64), 16, seed=23)
+    lives = torch.zeros(good.rows, dtype=torch.bool, device="cuda")
+    lives[:q] = True                                   # sequence 0 is untouched below
+    for what, value in (("table", -5), ("table", 10 ** 6), ("kv_len", 10 ** 6), ("kv_len", -3),
+                        ("q_start", 10 ** 6)):
+        step = Step([(q, 150), (q, 90)], (8, 2, 64), 16, seed=23)
+        if what == "table":
+            step.table[1, 2] = value
+        elif what == "kv_len":
+            step.kv_len[1] = value
+        else:
+            step.q_start[2] = value
+        y = step.attend()
+        status, word = bl.bitlinear_get_fault()
+        assert status == bl.BITLINEAR_ERR_INDEX and word == 2, (what, value, status, word)
+        good.check_attention(y, rows=lives)
+    assert bl.bitlinear_get_fault() == (bl.BITLINEAR_OK, 0)
