@@ -131,47 +131,106 @@ size_t parts_layout(int64_t workers, int64_t row_cap, int64_t head_dim, char *ba
     return hb + mb + ob;
 }
 
-constexpr int kRowsKernelMax = 32;                   // rows of its largest item
+constexpr int kRowsKernelMax = 32;                   // rows of the rows kernel's largest item
 
-template <int D, int MT>
-cudaError_t launch_attn_rows(const attn::Maps &maps, const attn::Params &p, int grid, int dev,
-                             cudaStream_t st)
+// Workspace: the parts of the rows kernel, then those of the chunk kernel,
+// which only sequences of more rows than the rows kernel's items reach.
+struct AttnLayout {
+    paged::Parts rows, chunk;
+    size_t bytes;
+};
+
+AttnLayout attn_layout(int64_t rows, int64_t head_dim, char *base)
 {
-    constexpr int smem = attn::rows::Cfg<D>::SMEM_BYTES;
-    cudaError_t e = allow_smem<attn::rows::attn_rows_kernel<D, MT>>(dev, smem);
-    if (e == cudaSuccess)
-        e = launch(attn::rows::attn_rows_kernel<D, MT>, dim3(grid), dim3(attn::rows::THREADS),
-                   static_cast<size_t>(smem), st, maps, p);
-    return e;
+    AttnLayout l{};
+    l.bytes = parts_layout(kAttnMaxGrid * attn::rows::WARPS, std::min<int64_t>(rows, kRowsKernelMax),
+                           head_dim, base, &l.rows);
+    if (rows > kRowsKernelMax)
+        l.bytes += parts_layout(kAttnMaxGrid, std::min<int64_t>(rows, attn::chunk::BM), head_dim,
+                                base + l.bytes, &l.chunk);
+    return l;
 }
 
-template <int D>
-int run_attention(attn::Params p, const bitlinear_kv_cache &cache, int64_t max_rows, char *ws,
-                  const DeviceInfo &dev, cudaStream_t st)
+int launch_merge(const attn::Params &p, int64_t head_dim, int workers, int item_rows,
+                 cudaStream_t st)
 {
-    const int64_t rows = static_cast<int64_t>(p.work.seqs.tokens) * p.work.group;
-    const int grid = std::min(dev.sms, kAttnMaxGrid);
-    p.cache_rows = static_cast<int>(cache.pages * cache.kv_heads * cache.page);
-    p.wait_limit_ns = kWaitLimitNs;
+    const attn::MergeParams m{p.parts, p.y,    p.y_stride, p.lse,
+                              p.q_heads, p.work, workers,    item_rows};
+    const dim3 grid(workers, item_rows / 16), block(attn::MERGE_THREADS);
+    return launch_status(head_dim == 64 ? launch(attn::merge_kernel<64>, grid, block, 0, st, m)
+                                        : launch(attn::merge_kernel<128>, grid, block, 0, st, m));
+}
+
+template <int D, int MT>
+int run_attn_rows(const attn::Params &p, const bitlinear_kv_cache &cache, const DeviceInfo &dev,
+                  cudaStream_t st)
+{
+    constexpr int smem = attn::rows::Cfg<D>::SMEM_BYTES;
     attn::Maps maps{};
     const uint32_t box = static_cast<uint32_t>(std::min<int64_t>(cache.page, attn::rows::BN));
     if (!make_map_cache(&maps.k, cache.k_dev, cache, box) ||
         !make_map_cache(&maps.v, cache.v_dev, cache, box))
         return BITLINEAR_ERR_CUDA;
-    parts_layout(kAttnMaxGrid * attn::rows::WARPS, std::min<int64_t>(rows, kRowsKernelMax), D, ws,
-                 &p.parts);
+    const int grid = std::min(dev.sms, kAttnMaxGrid);
+    cudaError_t e = allow_smem<attn::rows::attn_rows_kernel<D, MT>>(dev.id, smem);
+    if (e == cudaSuccess)
+        e = launch(attn::rows::attn_rows_kernel<D, MT>, dim3(grid), dim3(attn::rows::THREADS),
+                   static_cast<size_t>(smem), st, maps, p);
+    const int rc = launch_status(e);
+    return rc != BITLINEAR_OK ? rc : launch_merge(p, D, grid * attn::rows::WARPS, 16 * MT, st);
+}
+
+template <int D>
+int run_attn_chunk(const attn::Params &p, const bitlinear_kv_cache &cache, const DeviceInfo &dev,
+                   cudaStream_t st)
+{
+    constexpr int smem = attn::chunk::Cfg<D>::SMEM_BYTES;
+    attn::Maps maps{};
+    const uint32_t box = static_cast<uint32_t>(std::min<int64_t>(cache.page, attn::chunk::BN));
+    if (!make_map_cache(&maps.k, cache.k_dev, cache, box) ||
+        !make_map_cache(&maps.v, cache.v_dev, cache, box))
+        return BITLINEAR_ERR_CUDA;
+    const int grid = std::min(dev.sms, kAttnMaxGrid);
+    cudaError_t e = allow_smem<attn::chunk::attn_chunk_kernel<D>>(dev.id, smem);
+    if (e == cudaSuccess)
+        e = launch(attn::chunk::attn_chunk_kernel<D>, dim3(grid), dim3(attn::chunk::THREADS),
+                   static_cast<size_t>(smem), st, maps, p);
+    const int rc = launch_status(e);
+    return rc != BITLINEAR_OK ? rc : launch_merge(p, D, grid, attn::chunk::BM, st);
+}
+
+// The kernels of a step, by the rows (new tokens times query heads per key
+// head) that its longest sequence can have. Up to 32, only the rows kernel
+// runs. Otherwise sequences of more rows than one of its items go to the chunk
+// kernel, the others to the rows kernel; when the step has at least 64 rows a
+// sequence on average the chunk kernel takes all of them in one launch.
+template <int D>
+int run_attention(attn::Params p, const bitlinear_kv_cache &cache, int64_t max_rows, char *ws,
+                  const DeviceInfo &dev, cudaStream_t st)
+{
+    const int64_t rows = static_cast<int64_t>(p.work.seqs.tokens) * p.work.group;
+    const AttnLayout layout = attn_layout(rows, D, ws);
+    p.cache_rows = static_cast<int>(cache.pages * cache.kv_heads * cache.page);
+    p.wait_limit_ns = kWaitLimitNs;
     p.work.min_rows = 1;
     p.work.max_rows = INT_MAX;
-    const bool small = max_rows <= 16;
-    cudaError_t e = small ? launch_attn_rows<D, 1>(maps, p, grid, dev.id, st)
-                          : launch_attn_rows<D, 2>(maps, p, grid, dev.id, st);
-    if (e != cudaSuccess)
-        return launch_status(e);
-    attn::MergeParams mp{p.parts, p.y, p.y_stride, p.lse, p.q_heads, p.work,
-                         grid * attn::rows::WARPS, small ? 16 : 32};
-    e = launch(attn::merge_kernel<D>, dim3(grid * attn::rows::WARPS, small ? 2 : 4),
-               dim3(attn::MERGE_THREADS), 0, st, mp);
-    return launch_status(e);
+    p.parts = layout.rows;
+    if (max_rows <= 16)
+        return run_attn_rows<D, 1>(p, cache, dev, st);
+    if (max_rows <= kRowsKernelMax)
+        return run_attn_rows<D, 2>(p, cache, dev, st);
+    if (rows < 64 * static_cast<int64_t>(p.work.seqs.seqs)) {
+        const bool small = p.work.group <= 16;
+        p.work.max_rows = small ? 16 : 32;
+        const int rc = small ? run_attn_rows<D, 1>(p, cache, dev, st)
+                             : run_attn_rows<D, 2>(p, cache, dev, st);
+        if (rc != BITLINEAR_OK)
+            return rc;
+        p.work.min_rows = p.work.max_rows + 1;
+        p.work.max_rows = INT_MAX;
+    }
+    p.parts = layout.chunk;
+    return run_attn_chunk<D>(p, cache, dev, st);
 }
 
 }  // namespace
@@ -250,9 +309,7 @@ extern "C" size_t bitlinear_workspace_bytes_attention(int64_t tokens, int64_t se
         return SIZE_MAX;
     if (tokens == 0 || seqs == 0)
         return 0;
-    const int64_t rows = tokens * (q_heads / kv_heads);
-    return parts_layout(kAttnMaxGrid * attn::rows::WARPS, std::min<int64_t>(rows, kRowsKernelMax),
-                        head_dim, nullptr, nullptr);
+    return attn_layout(tokens * (q_heads / kv_heads), head_dim, nullptr).bytes;
 }
 
 extern "C" int bitlinear_paged_attention(const void *q_dev, int64_t q_stride, int64_t tokens,

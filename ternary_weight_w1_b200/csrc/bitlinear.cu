@@ -27,6 +27,7 @@
 #include "paged.cuh"
 #include "rope_append.cuh"
 #include "attn_rows.cuh"
+#include "attn_chunk.cuh"
 
 using namespace bitlinear;
 
