@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -81,18 +82,6 @@ class _Problem(ctypes.Structure):
     _fields_ = [("x_dev", ctypes.c_void_p), ("M", ctypes.c_int64), ("K", ctypes.c_int64),
                 ("N", ctypes.c_int64), ("packed_dev", ctypes.c_void_p),
                 ("gamma", ctypes.c_float), ("y_dev", ctypes.c_void_p)]
-
-
-class _KVCache(ctypes.Structure):
-    _fields_ = [("k_dev", ctypes.c_void_p), ("v_dev", ctypes.c_void_p),
-                ("pages", ctypes.c_int64), ("kv_heads", ctypes.c_int64),
-                ("page", ctypes.c_int64), ("head_dim", ctypes.c_int64)]
-
-
-class _Seqs(ctypes.Structure):
-    _fields_ = [("q_start_dev", ctypes.c_void_p), ("kv_len_dev", ctypes.c_void_p),
-                ("page_table_dev", ctypes.c_void_p), ("seqs", ctypes.c_int64),
-                ("table_cols", ctypes.c_int64)]
 
 
 _lib = None
@@ -560,28 +549,68 @@ def _ffn_width(packed, K: int) -> int:
 
 
 # ------------------------------------------------- attention on a paged cache
+#
+# A decode step makes these calls once per layer around kernels of a few
+# microseconds, so their argument checks are written for speed: the common
+# case is decided by a few attribute reads per tensor, and only a tensor that
+# fails them goes through _Args, which finds the error or accepts it.
 
-def _paged(a: _Args, k_cache, v_cache, q_start, kv_len, page_table):
-    """The cache and sequence descriptors of one call (k_cache and v_cache
-    [pages][kv_heads][page][head_dim] bf16; q_start [S + 1], kv_len [S] and
-    page_table [S][columns] int32)."""
-    import torch
-    if k_cache.dim() != 4:
+_CACHE = struct.Struct("=2Q4q")        # bitlinear_kv_cache
+_SEQS = struct.Struct("=3Q2q")         # bitlinear_seqs
+
+
+def _dev(t, name: str, dtype, cur: int) -> int:
+    """Address of a contiguous tensor on the current device ``cur``."""
+    if t.get_device() == cur and t.dtype is dtype and t.is_contiguous():
+        return t.data_ptr()
+    return _Args().ptr(t, name, dtype)
+
+
+def _head_rows(t, name: str, T, heads, D: int, cur: int, dtype):
+    """(address, row stride, heads) of a bf16 tensor of T rows of whole heads,
+    [T][heads * D] or [T][heads][D] (T or heads None: any)."""
+    shape = t.shape
+    n = len(shape)
+    got = shape[1] if n == 3 and shape[2] == D else shape[1] // D if n == 2 else 0
+    if (got == heads or heads is None and got > 0) and (T is None or shape[0] == T) and (
+            t.get_device() == cur and t.dtype is dtype and t.is_contiguous()
+            and (n == 3 or got * D == shape[1])):
+        return t.data_ptr(), got * D, got
+    if T is not None and n > 0 and shape[0] != T:
+        raise ValueError(f"{name} must have {T} rows, got {shape[0]}")
+    return _Args().rows(t, name, heads, D)
+
+
+def _paged(k_cache, v_cache, q_start, kv_len, page_table, cur: int, torch):
+    """(kv_heads, head_dim, sequences, the packed bitlinear_kv_cache and
+    bitlinear_seqs) of one call: k_cache and v_cache [pages][kv_heads][page]
+    [head_dim] bf16, q_start [S + 1], kv_len [S] and page_table [S][columns]
+    int32."""
+    shape = k_cache.shape
+    if len(shape) != 4:
         raise ValueError("k_cache must be [pages][kv_heads][page][head_dim], got "
-                         f"{tuple(k_cache.shape)}")
+                         f"{tuple(shape)}")
+    pages, kv_heads, page, D = shape
+    if D != 64 and D != 128:
+        raise BitLinearError(BITLINEAR_ERR_SHAPE, f"k_cache with head_dim {D}")
+    if v_cache.shape != shape:
+        raise ValueError(f"v_cache must have shape {tuple(shape)}, got {tuple(v_cache.shape)}")
     if page_table.dim() != 2:
         raise ValueError(f"page_table must be [S][columns], got {tuple(page_table.shape)}")
     S, cols = page_table.shape
-    pages, kv_heads, page, head_dim = k_cache.shape
-    if head_dim not in (64, 128):
-        raise BitLinearError(BITLINEAR_ERR_SHAPE, f"k_cache with head_dim {head_dim}")
-    cache = _KVCache(a.ptr(k_cache, "k_cache", torch.bfloat16),
-                     a.ptr(v_cache, "v_cache", torch.bfloat16, k_cache.shape),
-                     pages, kv_heads, page, head_dim)
-    seqs = _Seqs(a.ptr(q_start, "q_start", torch.int32, (S + 1,)),
-                 a.ptr(kv_len, "kv_len", torch.int32, (S,)),
-                 a.ptr(page_table, "page_table", torch.int32), S, cols)
-    return cache, seqs
+    if q_start.shape != (S + 1,) or kv_len.shape != (S,):
+        raise ValueError(f"q_start and kv_len must have shapes ({S + 1},) and ({S},), got "
+                         f"{tuple(q_start.shape)} and {tuple(kv_len.shape)}")
+    bf16, i32 = torch.bfloat16, torch.int32
+    return (kv_heads, D, S,
+            _CACHE.pack(_dev(k_cache, "k_cache", bf16, cur), _dev(v_cache, "v_cache", bf16, cur),
+                        pages, kv_heads, page, D),
+            _SEQS.pack(_dev(q_start, "q_start", i32, cur), _dev(kv_len, "kv_len", i32, cur),
+                       _dev(page_table, "page_table", i32, cur), S, cols))
+
+
+def _raw_stream(stream, cur: int, torch) -> int:
+    return torch._C._cuda_getCurrentRawStream(cur) if stream is None else stream.cuda_stream
 
 
 def _new(t, stream, shape=None, dtype=None):
@@ -608,28 +637,28 @@ def bitlinear_rope_append(q, k, v, k_cache, v_cache, q_start, kv_len, page_table
     fp32. Row i of sequence s (rows q_start[s] .. q_start[s + 1]) stands at
     position kv_len[s] - its rows + i. Returns the rotated queries (``q_out``,
     which may be ``q``; rows of no sequence are not written)."""
-    a = _Args()
     import torch
-    cache, seqs = _paged(a, k_cache, v_cache, q_start, kv_len, page_table)
-    D = cache.head_dim
-    qp, qs, heads = a.rows(q, "q", None, D)
-    kp, ks, _ = a.rows(k, "k", cache.kv_heads, D)
-    vp, vs, _ = a.rows(v, "v", cache.kv_heads, D)
-    if k.shape[0] != q.shape[0] or v.shape[0] != q.shape[0]:
-        raise ValueError(f"q, k and v must have the same rows, got {q.shape[0]}, {k.shape[0]}, "
-                         f"{v.shape[0]}")
+    cur = torch._C._cuda_getDevice() if k_cache.is_cuda else -2
+    bf16, f32 = torch.bfloat16, torch.float32
+    kv_heads, D, _, cache, seqs = _paged(k_cache, v_cache, q_start, kv_len, page_table, cur, torch)
+    qp, qs, heads = _head_rows(q, "q", None, None, D, cur, bf16)
+    T = q.shape[0]
+    kp, ks, _ = _head_rows(k, "k", T, kv_heads, D, cur, bf16)
+    vp, vs, _ = _head_rows(v, "v", T, kv_heads, D, cur, bf16)
     if q_out is None:
         q_out = _new(q, stream)
-    op, os_, _ = a.rows(q_out, "q_out", heads, D)
-    if q_out.shape[0] != q.shape[0]:
-        raise ValueError(f"q_out must have {q.shape[0]} rows, got {q_out.shape[0]}")
-    _check(lib().bitlinear_rope_append(
-               qp, qs, kp, ks, vp, vs, q.shape[0], heads, ctypes.addressof(cache),
-               ctypes.addressof(seqs), a.ptr(inv_freq, "inv_freq", torch.float32, (D // 2,)),
-               1 if interleaved else 0, a.ptr(q_gain, "q_gain", torch.float32, (D,)),
-               a.ptr(k_gain, "k_gain", torch.float32, (D,)), float(eps), op, os_,
-               _stream(stream)),
-           "bitlinear_rope_append")
+    op, os_, _ = _head_rows(q_out, "q_out", T, heads, D, cur, bf16)
+    for t, name, n in ((inv_freq, "inv_freq", D // 2), (q_gain, "q_gain", D),
+                       (k_gain, "k_gain", D)):
+        if t is not None and t.shape != (n,):
+            raise ValueError(f"{name} must have shape ({n},), got {tuple(t.shape)}")
+    rc = lib().bitlinear_rope_append(
+        qp, qs, kp, ks, vp, vs, T, heads, cache, seqs, _dev(inv_freq, "inv_freq", f32, cur),
+        1 if interleaved else 0, None if q_gain is None else _dev(q_gain, "q_gain", f32, cur),
+        None if k_gain is None else _dev(k_gain, "k_gain", f32, cur), eps, op, os_,
+        _raw_stream(stream, cur, torch))
+    if rc:
+        _check(rc, "bitlinear_rope_append")
     return q_out
 
 
@@ -653,29 +682,29 @@ def bitlinear_paged_attention(q, k_cache, v_cache, q_start, kv_len, page_table, 
     ``bitlinear_workspace_bytes_attention`` bytes (allocated here when
     omitted). Returns ``y`` (bf16, shaped like ``q``; rows that see no key are
     zero, rows of no sequence are not written)."""
-    a = _Args()
     import torch
-    cache, seqs = _paged(a, k_cache, v_cache, q_start, kv_len, page_table)
-    D = cache.head_dim
-    qp, qs, heads = a.rows(q, "q", None, D)
+    cur = torch._C._cuda_getDevice() if k_cache.is_cuda else -2
+    bf16 = torch.bfloat16
+    kv_heads, D, S, cache, seqs = _paged(k_cache, v_cache, q_start, kv_len, page_table, cur, torch)
+    qp, qs, heads = _head_rows(q, "q", None, None, D, cur, bf16)
     T = q.shape[0]
     if y is None:
         y = _new(q, stream)
-    yp, ys, _ = a.rows(y, "y", heads, D)
-    if y.shape[0] != T:
-        raise ValueError(f"y must have {T} rows, got {y.shape[0]}")
-    need = bitlinear_workspace_bytes_attention(T, seqs.seqs, heads, cache.kv_heads, D)
-    if need == ctypes.c_size_t(-1).value:
-        raise BitLinearError(BITLINEAR_ERR_SHAPE, "bitlinear_workspace_bytes_attention")
-    if workspace is None and need > 0:
+    yp, ys, _ = _head_rows(y, "y", T, heads, D, cur, bf16)
+    if lse is not None and lse.shape != (T, heads):
+        raise ValueError(f"lse must have shape ({T}, {heads}), got {tuple(lse.shape)}")
+    if workspace is None:
+        need = bitlinear_workspace_bytes_attention(T, S, heads, kv_heads, D)
+        if need == ctypes.c_size_t(-1).value:
+            raise BitLinearError(BITLINEAR_ERR_SHAPE, "bitlinear_workspace_bytes_attention")
         workspace = _new(q, stream, (need,), torch.uint8)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().bitlinear_paged_attention(
-               qp, qs, T, heads, ctypes.addressof(cache), ctypes.addressof(seqs),
-               float(D ** -0.5 if scale is None else scale), int(window),
-               int(max_q_len or 0), yp, ys, a.ptr(lse, "lse", torch.float32, (T, heads)),
-               a.ptr(workspace, "workspace"), ws_bytes, _stream(stream)),
-           "bitlinear_paged_attention")
+    rc = lib().bitlinear_paged_attention(
+        qp, qs, T, heads, cache, seqs, D ** -0.5 if scale is None else scale, window,
+        max_q_len or 0, yp, ys, None if lse is None else _dev(lse, "lse", torch.float32, cur),
+        _dev(workspace, "workspace", torch.uint8, cur), workspace.numel(),
+        _raw_stream(stream, cur, torch))
+    if rc:
+        _check(rc, "bitlinear_paged_attention")
     return y
 
 

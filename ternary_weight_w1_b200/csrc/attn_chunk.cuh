@@ -2,22 +2,22 @@
 // prompts) on the fifth-generation tensor cores.
 //
 // An item is 256 rows of one sequence and key head in two halves of 128, each
-// a tcgen05.mma of M = 128. Per tile of 128 keys and half h:
+// a tcgen05.mma of M = 128. Per step of 64 keys and half h:
 //   S_h = Q_h K^T          both operands from shared memory, S_h in TMEM
 //   P_h = 2^(scale S_h - m) by four warps, one row per thread, bf16 back into
 //                          the columns of S_h
 //   O_h += P_h V           P_h from TMEM, V from shared memory as it lies there
 //                          (its channels contiguous: an MN-major operand)
-// The products of one half run while the other half's warps compute its
-// exponentials, which is what bounds the kernel: a tile takes 4 * 256 * 128 * D
-// flops of the tensor pipe and 256 * 128 exponentials, about as many clocks of
-// the special-function units at D = 128, and twice as many at D = 64.
+// Each half has two S buffers, which the two steps of a 128-key tile take in
+// turn: the products of one step run while the warps compute the exponentials
+// of the other, so neither waits for the other's latency. (With one buffer of
+// 128 keys, and the halves alone overlapping, a tile took 4580 clocks at D =
+// 128, of which the tensor pipe worked 45%.)
 //
 // One persistent block per SM. Warps 0-3 and 4-7 compute the halves' softmax,
-// warp 8 fetches keys and values through a ring of tiles, warp 9 issues the
-// products. S_h(j + 1) is issued after P_h V_j, and a commit covers all
-// products before it: a half's warps that see S_h(j + 1) know that O_h is at
-// rest, so they rescale it themselves when their row's maximum has grown.
+// warp 8 fetches keys and values through a ring of tiles, warps 9 and 10 issue
+// the products of one half each. A warp whose row's maximum has grown rescales its rows of O_h
+// itself, after the products of the previous step (its o_done).
 #pragma once
 
 #include "attn_rows.cuh"
@@ -28,18 +28,35 @@ namespace chunk {
 
 constexpr int BM = 256, HALF = 128;    // rows of an item, of a half
 constexpr int BN = 128;                // keys of a tile
+constexpr int STEP = 64;               // keys of a step: the tile's two halves
 constexpr int SOFTMAX_WARPS = 8;
-constexpr int THREADS = (SOFTMAX_WARPS + 2) * 32;
+constexpr int THREADS = (SOFTMAX_WARPS + 3) * 32;
 constexpr int TMEM_COLS = 512;
-
 template <int D>
 struct Cfg {
     static constexpr int CH = D / 64;                          // 64-channel column blocks
     static constexpr int Q_BYTES = HALF * D * 2;               // one half
     static constexpr int TILE_BYTES = BN * D * 2;              // keys or values of a tile
-    static constexpr int STAGES = D == 128 ? 5 : 8;
-    static constexpr int SMEM_BYTES = 1024 + 2 * Q_BYTES + STAGES * TILE_BYTES;
+    static constexpr int STAGES = D == 128 ? 4 : 8;
+    static constexpr int OUT_BYTES = 32 * 128;                 // staged output of one warp
+    static constexpr int SMEM_BYTES =
+        1024 + 2 * Q_BYTES + STAGES * TILE_BYTES + SOFTMAX_WARPS * OUT_BYTES;
 };
+
+// True in one lane of the warp. A branch on it (rather than on a lane number)
+// tells the compiler that a single lane runs the issuing code, so that the
+// descriptors go straight to the uniform registers that the instructions take
+// them from.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, e;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
 
 // D[tmem] (+)= A[smem] B[smem]^T, bf16 inputs, fp32 accumulator.
 __device__ __forceinline__ void umma_bf16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -88,6 +105,86 @@ __device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr, uint32_t 
     return d;
 }
 
+// Ties 32 registers of a TMEM load to what was waited for before it: their
+// readers cannot be moved in front.
+__device__ __forceinline__ void loaded32(uint32_t *r)
+{
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                   "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                   "+r"(r[30]), "+r"(r[31]));
+}
+
+// Two fp32 lanes of one 64-bit register: a multiply-add or an add of both is
+// one instruction.
+__device__ __forceinline__ uint64_t pair(float lo, float hi)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+
+__device__ __forceinline__ void unpair(uint64_t v, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// 2^x of two lanes on the multiply-add pipe, for -126 <= x < 127: x = n + f with
+// n the nearest integer (the low bits of x + 1.5 * 2^23), 2^f by the degree-4
+// polynomial of least relative error on [-1/2, 1/2] (2.7e-6, Remez exchange),
+// n added to its exponent. The special-function unit gives 16 results a clock
+// and SM and would bound the kernel alone; every fourth pair goes this way.
+__device__ __forceinline__ void exp2_poly2(uint64_t x, float &lo, float &hi)
+{
+    float a, b;
+    unpair(x, a, b);
+    x = pair(fmaxf(a, -126.0f), fmaxf(b, -126.0f));
+    const uint64_t r = add2(x, pair(12582912.0f, 12582912.0f));
+    const uint64_t f = add2(x, add2(pair(12582912.0f, 12582912.0f),
+                                    r ^ 0x8000000080000000ull));
+    uint64_t q = fma2(pair(0.009570102207362652f, 0.009570102207362652f), f,
+                      pair(0.05591785907745361f, 0.05591785907745361f));
+    q = fma2(q, f, pair(0.240247443318367f, 0.240247443318367f));
+    q = fma2(q, f, pair(0.6931217908859253f, 0.6931217908859253f));
+    q = fma2(q, f, pair(0.9999992847442627f, 0.9999992847442627f));
+    float n0, n1;
+    unpair(r, n0, n1);
+    unpair(q, lo, hi);
+    lo = __uint_as_float(__float_as_uint(lo) + (__float_as_uint(n0) << 23));
+    hi = __uint_as_float(__float_as_uint(hi) + (__float_as_uint(n1) << 23));
+}
+
+// 16 columns of the warp's 32 lanes, waited for.
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t *r)
 {
     asm volatile(
@@ -107,11 +204,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     using Cursor = paged::Cursor<BM, BN>;
 
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * C::STAGES + 9];
+    __shared__ __align__(8) uint64_t bars[2 * C::STAGES + 16];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_word;
 
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
     const uint32_t smem0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t q_smem = smem0;                             // [half][column block][row][128 B]
     const uint32_t ring = smem0 + 2 * C::Q_BYTES;              // [stage][column block][key][128 B]
@@ -121,58 +219,53 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto full = [&](int s) { return bar(s); };
     auto empty = [&](int s) { return bar(C::STAGES + s); };
     auto q_ready = [&](int h) { return bar(2 * C::STAGES + h); };
-    auto s_full = [&](int h) { return bar(2 * C::STAGES + 2 + h); };
-    auto p_ready = [&](int h) { return bar(2 * C::STAGES + 4 + h); };
-    auto o_full = [&](int h) { return bar(2 * C::STAGES + 6 + h); };
-    const uint32_t drain_bar = bar(2 * C::STAGES + 8);
+    auto o_done = [&](int h, int b) { return bar(2 * C::STAGES + 2 + 2 * h + b); };
+    auto s_full = [&](int h, int b) { return bar(2 * C::STAGES + 6 + 2 * h + b); };
+    auto p_ready = [&](int h, int b) { return bar(2 * C::STAGES + 10 + 2 * h + b); };
+    auto drain_bar = [&](int h) { return bar(2 * C::STAGES + 14 + h); };
 
     if (threadIdx.x == 0) {
         prefetch_tensormap(&maps.k);
         prefetch_tensormap(&maps.v);
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(full(s), 1);
-            mbar_init(empty(s), 1);
+            mbar_init(empty(s), 2);                            // both halves
         }
         for (int h = 0; h < 2; ++h) {
             mbar_init(q_ready(h), 4);
-            mbar_init(s_full(h), 1);
-            mbar_init(p_ready(h), 4);
-            mbar_init(o_full(h), 1);
+            mbar_init(drain_bar(h), 1);
+            for (int b = 0; b < 2; ++b) {
+                mbar_init(o_done(h, b), 1);
+                mbar_init(s_full(h, b), 1);
+                mbar_init(p_ready(h, b), 4);
+            }
         }
-        mbar_init(drain_bar, 1);
         fence_barrier_init();
         abort_word = 0;
     }
     if (warp == 9)
         tmem_alloc(smem_u32(&tmem_slot), TMEM_COLS);
-    pdl_wait();
-    pdl_launch_dependents();
-    const paged::Work &w = p.work;
-    paged::group_units<BM, BN>(w, warp, THREADS / 32, sums);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = tmem_slot;
-    int64_t per_head = 0;
-    for (int g = 0; g < (w.seqs.seqs + 31) / 32; ++g)
-        per_head += sums[g];
-    const int64_t units = per_head * w.kv_heads;
-    const int worker = blockIdx.x, workers = gridDim.x;
-    const int64_t base = units / workers, extra = units % workers;
-    const int64_t u0 = worker * base + min(static_cast<int64_t>(worker), extra);
-    const int64_t count = base + (worker < extra ? 1 : 0);
+    pdl_wait();
+    pdl_launch_dependents();
+    const paged::Work &w = p.work;
+    const int worker = blockIdx.x;
     Cursor cur;
-    if (count > 0)
-        cur.seek(w, sums, per_head, u0);
-    __syncthreads();                                           // sums is read; its memory is Q's
+    const int64_t count = paged::deal<BM, BN>(w, worker, gridDim.x, sums, cur);
+    if (w.seqs.seqs > 32)
+        __syncthreads();                                       // sums is read; its memory is Q's
 
     // The whole warp waits; false after a timeout anywhere in the block.
     auto wait = [&](uint32_t b, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_try_wait(b, parity)) ||
                warp_wait_bounded(b, parity, abort_flag, p.wait_limit_ns);
     };
-    // S_h at column h * 128 (P_h in its first 64 columns), O_h behind them.
-    auto s_tmem = [&](int h) { return tmem + h * 128; };
+    // S buffer b of half h at column h * 128 + b * 64 (P in its first 32), O_h
+    // behind them.
+    auto s_tmem = [&](int h, int b) { return tmem + h * 128 + b * STEP; };
     auto o_tmem = [&](int h) { return tmem + 256 + h * 128; };
     auto parts_tiles = [&](int64_t left) {
         const int64_t n = cur.t.end - cur.tile;
@@ -230,12 +323,17 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int s = 0; s < C::STAGES; ++s)
                 if ((armed >> s) & 1u)
                     drain_wait(full(s), s < st ? ph : ph ^ 1u, p.wait_limit_ns);
-    } else if (warp == 9) {
-        // ======================================================= products
-        constexpr uint32_t S_IDESC = idesc_bf16(HALF, BN, false);
+    } else if (warp == 9 || warp == 10) {
+        // ============================================== products of half h
+        constexpr uint32_t S_IDESC = idesc_bf16(HALF, STEP, false);
         constexpr uint32_t O_IDESC = idesc_bf16(HALF, D, true);
+        constexpr uint32_t STEP_OFF = STEP * 128 / 16;         // 64 keys further, in 16 bytes
+        const int h = warp - 9;
+        const uint64_t q_desc = smem_desc_k128_sw128(q_smem + h * C::Q_BYTES);
+        const uint64_t k_desc = smem_desc_k128_sw128(ring);
+        const uint64_t v_desc = smem_desc_mn_sw128(ring, BN * 128);
         int st = 0;
-        uint32_t ph = 0, q_ph[2] = {0, 0}, p_ph[2] = {0, 0};
+        uint32_t ph = 0, q_ph = 0, p_ph = 0;
         bool ok = true;
         auto next_stage = [&]() {
             if (++st == C::STAGES) {
@@ -243,105 +341,156 @@ __global__ void __launch_bounds__(THREADS, 1)
                 ph ^= 1u;
             }
         };
-        auto scores = [&](int h, int stage) {
-            const uint64_t a = smem_desc_k128_sw128(q_smem + h * C::Q_BYTES);
-            const uint64_t b = smem_desc_k128_sw128(ring + stage * C::TILE_BYTES);
+        auto scores = [&](int b, int stage) {
+            const uint64_t k = k_desc + stage * (C::TILE_BYTES / 16) + b * STEP_OFF;
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
+            for (int i = 0; i < D / 16; ++i) {
                 // 16 channels are 32 bytes of a 128-byte row, 64 a column block
-                const uint64_t off = (k >> 2) * (HALF * 128 / 16) + (k & 3) * 2;
-                umma_bf16_ss(s_tmem(h), a + off, b + off, S_IDESC, k > 0);
+                const uint64_t off = (i >> 2) * (HALF * 128 / 16) + (i & 3) * 2;
+                umma_bf16_ss(s_tmem(h, b), q_desc + off, k + off, S_IDESC, i > 0);
             }
-            umma_commit(s_full(h));
+            umma_commit(s_full(h, b));
         };
         while (ok && left > 0) {
-            const int nt = parts_tiles(left), nh = halves_of();
-            int k_stage = st;
-            ok = wait(full(st), ph);
-            next_stage();
-            for (int h = 0; ok && h < nh; ++h) {
-                ok = wait(q_ready(h), q_ph[h]);
-                q_ph[h] ^= 1u;
-                tc_fence_after_sync();
-                if (ok && lane == 0)
-                    scores(h, k_stage);
-            }
-            if (ok && lane == 0)
-                umma_commit(empty(k_stage));
-            for (int j = 0; ok && j < nt; ++j) {
-                const int v_stage = st;
-                ok = wait(full(st), ph);
-                next_stage();
+            const int nt = parts_tiles(left);
+            if (h < halves_of()) {
+                int k_stage = st;
+                ok = wait(q_ready(h), q_ph) && wait(full(st), ph);
+                q_ph ^= 1u;
                 if (!ok)
                     break;
-                const int key0 = (cur.tile + j) * BN;
-                const int skip = max(cur.t.klo - key0, 0), upto = min(cur.t.khi - key0, BN);
-                if (skip > 0 || upto < BN) {
-                    // slots that hold no key of the sequence may hold anything,
-                    // and 0 * NaN is NaN: their values become zeros
-                    for (int i = lane; i < BN * 8 * C::CH; i += 32) {
-                        const int key = (i >> 3) & (BN - 1);
-                        if (key < skip || key >= upto)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                             ring + v_stage * C::TILE_BYTES + i * 16),
-                                         "r"(0)
-                                         : "memory");
-                    }
-                    fence_proxy_async();
-                    __syncwarp();
+                next_stage();
+                tc_fence_after_sync();
+                if (elect_one()) {
+                    scores(0, k_stage);
+                    scores(1, k_stage);
+                    umma_commit(empty(k_stage));
                 }
-                for (int h = 0; ok && h < nh; ++h) {
-                    ok = wait(p_ready(h), p_ph[h]);
-                    p_ph[h] ^= 1u;
+                __syncwarp();
+                for (int j = 0; j < nt; ++j) {
+                    const int v_stage = st;
+                    ok = wait(full(st), ph);
                     if (!ok)
                         break;
-                    tc_fence_after_sync();
-                    if (lane == 0) {
-                        const uint64_t b =
-                            smem_desc_mn_sw128(ring + v_stage * C::TILE_BYTES, BN * 128);
-#pragma unroll
-                        for (int k = 0; k < BN / 16; ++k)      // 16 keys: two 1024-byte atoms
-                            umma_bf16_ts(o_tmem(h), s_tmem(h) + k * 8, b + k * (2048 / 16), O_IDESC,
-                                         j > 0 || k > 0);
-                        if (h == nh - 1)
-                            umma_commit(empty(v_stage));
-                        if (j + 1 == nt)
-                            umma_commit(o_full(h));
-                    }
-                    __syncwarp();
-                    if (j + 1 < nt) {
-                        if (h == 0) {
-                            k_stage = st;
-                            ok = wait(full(st), ph);
-                            next_stage();
-                            if (!ok)
-                                break;
+                    next_stage();
+                    const int key0 = (cur.tile + j) * BN;
+                    const int skip = max(cur.t.klo - key0, 0), upto = min(cur.t.khi - key0, BN);
+                    if (skip > 0 || upto < BN) {
+                        // slots that hold no key of the sequence may hold
+                        // anything, and 0 * NaN is NaN: their values become
+                        // zeros (the halves' warps write the same ones)
+                        for (int i = lane; i < BN * 8 * C::CH; i += 32) {
+                            const int key = (i >> 3) & (BN - 1);
+                            if (key < skip || key >= upto)
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                                 ring + v_stage * C::TILE_BYTES + i * 16),
+                                             "r"(0)
+                                             : "memory");
                         }
-                        if (lane == 0) {
-                            scores(h, k_stage);
-                            if (h == nh - 1)
-                                umma_commit(empty(k_stage));
-                        }
+                        fence_proxy_async();
                         __syncwarp();
                     }
+                    const bool more = j + 1 < nt;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        ok = ok && wait(p_ready(h, b), p_ph);
+                        if (!ok)
+                            break;
+                        tc_fence_after_sync();
+                        if (elect_one()) {
+                            const uint64_t v =
+                                v_desc + v_stage * (C::TILE_BYTES / 16) + b * STEP_OFF;
+#pragma unroll
+                            for (int i = 0; i < STEP / 16; ++i)    // 16 keys: two 1024-byte atoms
+                                umma_bf16_ts(o_tmem(h), s_tmem(h, b) + i * 8, v + i * (2048 / 16),
+                                             O_IDESC, j > 0 || b > 0 || i > 0);
+                            umma_commit(o_done(h, b));
+                            if (b == 1)
+                                umma_commit(empty(v_stage));
+                        }
+                        __syncwarp();
+                        if (more) {
+                            if (b == 0) {
+                                k_stage = st;
+                                ok = wait(full(st), ph);
+                                if (!ok)
+                                    break;
+                                next_stage();
+                            }
+                            if (elect_one()) {
+                                scores(b, k_stage);
+                                if (b == 1)
+                                    umma_commit(empty(k_stage));
+                            }
+                            __syncwarp();
+                        }
+                    }
+                    p_ph ^= 1u;
+                    if (!ok)
+                        break;
+                }
+            } else {
+                // the item has no rows in this half: give its tiles back
+                for (int j = 0; ok && j < 2 * nt; ++j) {
+                    ok = wait(full(st), ph);
+                    if (ok && lane == 0)
+                        mbar_arrive(empty(st));
+                    next_stage();
                 }
             }
             left -= nt;
             if (ok && left > 0)
                 cur.next_item(w);
         }
-        if (lane == 0) {                                       // nothing in flight at the end
-            umma_commit(drain_bar);
-            drain_wait(drain_bar, 0u, p.wait_limit_ns);
+        if (elect_one()) {                                     // nothing in flight at the end
+            umma_commit(drain_bar(h));
+            drain_wait(drain_bar(h), 0u, p.wait_limit_ns);
         }
-    } else {
+        __syncwarp();
+    } else if (warp < SOFTMAX_WARPS) {
         // ======================================================== softmax
         const int h = warp >> 2;
         const int r = h * HALF + (warp & 3) * 32 + lane;       // row of the item
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t s_addr = s_tmem(h) + lane_off, o_addr = o_tmem(h) + lane_off;
-        uint32_t s_ph = 0, o_ph = 0;
-        bool ok = true;
+        const uint32_t s_addr = s_tmem(h, 0) + lane_off, o_addr = o_tmem(h) + lane_off;
+        const uint32_t out = ring + C::STAGES * C::TILE_BYTES + warp * C::OUT_BYTES;
+        const int row0 = h * HALF + (warp & 3) * 32;           // the warp's first row of the item
+        uint32_t ph = 0;                                       // parity of the tile's barriers
+        bool ok = true, q_there = false;
+        // address of channel 0 of item row i of cursor c in a tensor of rows
+        auto row_of = [&](const Cursor &c, int i, int64_t stride) {
+            const int rr = c.m * BM + i;
+            const int tok = w.by_group(rr);
+            return (c.v.q0 + tok) * stride + (c.h * w.group + rr - tok * w.group) * D;
+        };
+        // The warp's 32 rows, D / 8 lanes a row, so that a load covers whole lines.
+        auto load_q = [&](const Cursor &c) {
+            constexpr int PER = D / 8;
+            const int rows = c.v.qlen * w.group - c.m * BM;
+            uint4 x[PER];
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int at = row0 + (i * 32 + lane) / PER;
+                x[i] = at < rows ? __ldg(reinterpret_cast<const uint4 *>(
+                                             p.q + row_of(c, at, p.q_stride)) +
+                                         lane % PER)
+                                 : make_uint4(0, 0, 0, 0);
+            }
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int at = row0 - h * HALF + (i * 32 + lane) / PER, ch = lane % PER;
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 q_smem + h * C::Q_BYTES + (ch >> 3) * (HALF * 128) + at * 128 +
+                                 (((ch & 7) ^ (at & 7)) << 4)),
+                             "r"(x[i].x), "r"(x[i].y), "r"(x[i].z), "r"(x[i].w)
+                             : "memory");
+            }
+            fence_proxy_async();
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(q_ready(h));
+        };
         while (ok && left > 0) {
             const int nt = parts_tiles(left);
             const bool from_start = cur.tile == cur.t.begin;
@@ -349,64 +498,56 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int rows = min(BM, cur.v.qlen * w.group - cur.m * BM);
             const int slot = 2 * worker + (from_start ? 1 : 0);
             const bool whole = from_start && to_end;
+            const bool active = h < halves_of();
             if (!whole)
-                head[from_start ? 1 : 0] = paged::PartHeader{to_end ? 2 : 1, cur.s, cur.m, cur.h};
-            if (h < halves_of()) {
-                const int rr = cur.m * BM + r;
-                const int tok = rr / w.group;
-                const int hq = cur.h * w.group + rr - tok * w.group;
+                head[from_start ? 1 : 0] = paged::PartHeader{rows, to_end ? 0 : 1, cur.v.q0, cur.h + w.kv_heads * cur.m};
+            const int rr = cur.m * BM + r;
+            const int tok = w.by_group(rr);
+            float m = -INFINITY, l = 0.0f;
+            if (active) {
+                if (!q_there)
+                    load_q(cur);
                 const int seen_hi = cur.v.kv - cur.v.qlen + tok;     // last key the row sees
-                const int64_t row = cur.v.q0 + tok;
-                {
-                    const uint4 *src =
-                        reinterpret_cast<const uint4 *>(p.q + row * p.q_stride + hq * D);
-                    const uint32_t dst = q_smem + h * C::Q_BYTES + (r - h * HALF) * 128;
-#pragma unroll
-                    for (int c = 0; c < D / 8; ++c) {
-                        const uint4 x = r < rows ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                         dst + (c >> 3) * (HALF * 128) + (((c & 7) ^ (r & 7)) << 4)),
-                                     "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
-                                     : "memory");
-                    }
-                    fence_proxy_async();
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(q_ready(h));
-                }
                 // keys that every row of this warp sees: tiles inside need no mask
                 const int all_hi = __shfl_sync(0xffffffffu, seen_hi, 0);
                 const int all_lo =
                     w.window > 0 ? __shfl_sync(0xffffffffu, seen_hi, 31) - w.window + 1 : 0;
-                float m = -INFINITY, l = 0.0f;
-                for (int j = 0; j < nt; ++j) {
-                    if (!wait(s_full(h), s_ph)) {
+                for (int j = 0; j < 2 * nt; ++j) {
+                    const int b = j & 1;
+                    if (!wait(s_full(h, b), ph)) {
                         ok = false;
                         break;
                     }
-                    s_ph ^= 1u;
                     tc_fence_after_sync();
-                    uint32_t s[BN];
+                    uint32_t s[STEP];
 #pragma unroll
-                    for (int c = 0; c < BN / 32; ++c)
-                        tmem_ld_32x32b_x32(s_addr + c * 32,
+                    for (int c = 0; c < STEP / 32; ++c)
+                        tmem_ld_32x32b_x32(s_addr + b * STEP + c * 32,
                                            *reinterpret_cast<uint32_t(*)[32]>(s + c * 32));
                     tmem_ld_wait();
-                    const int key0 = (cur.tile + j) * BN;
-                    if (key0 + BN - 1 > all_hi || key0 < all_lo) {
+#pragma unroll
+                    for (int c = 0; c < STEP / 32; ++c)
+                        loaded32(s + c * 32);
+                    const int key0 = cur.tile * BN + j * STEP;
+                    const bool masked = key0 + STEP - 1 > all_hi || key0 < all_lo;
+                    if (masked) {
                         const int hi = seen_hi - key0;
                         const int lo = w.window > 0 ? hi - w.window : -1;
 #pragma unroll
-                        for (int i = 0; i < BN; ++i)
+                        for (int i = 0; i < STEP; ++i)
                             if (i > hi || i <= lo)
                                 s[i] = 0xff800000u;
                     }
-                    float top = -INFINITY;
+                    float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < BN; i += 2)
-                        top = fmaxf(top, fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
-                    top *= p.scale_log2;
+                    for (int i = 0; i < STEP; i += 8)
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            t4[k] = fmaxf(fmaxf(__uint_as_float(s[i + 2 * k]),
+                                                __uint_as_float(s[i + 2 * k + 1])),
+                                          t4[k]);
+                    const float top =
+                        fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * p.scale_log2;
                     const bool raise = top > m + RESCALE_AT;           // also from -inf
                     if (__any_sync(0xffffffffu, raise)) {
                         const float f = raise ? exp2_approx(m - top) : 1.0f;
@@ -414,86 +555,151 @@ __global__ void __launch_bounds__(THREADS, 1)
                             m = top;
                         l *= f;
                         if (j > 0) {
+                            // O_h rests after the last step's products (those of
+                            // the step before went ahead of this step's scores)
+                            if (!wait(o_done(h, b ^ 1), b == 1 ? ph : ph ^ 1u)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after_sync();
+#pragma unroll 1
+                            for (int c = 0; c < D / 16; ++c) {
+                                uint32_t o[16];
+                                tmem_ld_x16(o_addr + c * 16, o);
 #pragma unroll
-                            for (int c = 0; c < D / 32; ++c) {
-                                uint32_t o[32];
-                                tmem_ld_32x32b_x32(o_addr + c * 32, o);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int i = 0; i < 32; ++i)
+                                for (int i = 0; i < 16; ++i)
                                     o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                tmem_st_32x32b_x32(o_addr + c * 32, o);
+                                tmem_st_x16(o_addr + c * 16, o);
                             }
                         }
                     }
+                    ph ^= static_cast<uint32_t>(b);
                     const float sub = m == -INFINITY ? 0.0f : m;
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    const uint64_t scale2 = pair(p.scale_log2, p.scale_log2);
+                    const uint64_t sub2 = pair(-sub, -sub);
+                    uint64_t sum[4] = {0, 0, 0, 0};
+                    auto weights = [&](auto exact) {
 #pragma unroll
-                    for (int c = 0; c < BN / 32; ++c) {
-                        uint32_t e[16];
+                        for (int c = 0; c < STEP / 32; ++c) {
+                            uint32_t e[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float a = exp2_approx(
-                                fmaf(__uint_as_float(s[c * 32 + 2 * i]), p.scale_log2, -sub));
-                            const float b = exp2_approx(
-                                fmaf(__uint_as_float(s[c * 32 + 2 * i + 1]), p.scale_log2, -sub));
-                            sum[i & 3] += a + b;
-                            e[i] = pack_bf16(a, b);
+                            for (int i = 0; i < 16; ++i) {
+                                const uint64_t x =
+                                    fma2(pair(__uint_as_float(s[c * 32 + 2 * i]),
+                                              __uint_as_float(s[c * 32 + 2 * i + 1])),
+                                         scale2, sub2);
+                                float a, b;
+                                if (!decltype(exact)::value && i % 4 == 3) {
+                                    exp2_poly2(x, a, b);
+                                } else {
+                                    unpair(x, a, b);
+                                    a = exp2_approx(a);
+                                    b = exp2_approx(b);
+                                }
+                                sum[i & 3] = add2(sum[i & 3], pair(a, b));
+                                e[i] = pack_bf16(a, b);
+                            }
+                            tmem_st_x16(s_addr + b * STEP + c * 16, e);
                         }
-                        tmem_st_x16(s_addr + c * 16, e);
-                    }
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    };
+                    // a masked score is -inf and must weigh exactly nothing
+                    if (masked)
+                        weights(std::true_type{});
+                    else
+                        weights(std::false_type{});
                     tmem_st_wait();
                     tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(p_ready(h));
+                        mbar_arrive(p_ready(h, b));
+                    float a, c;
+                    unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, c);
+                    l += a + c;
                 }
-                if (!ok || !wait(o_full(h), o_ph)) {
+            }
+            if (!ok)
+                break;
+            // the next item's queries go ahead of this one's output: its last
+            // scores have been read, so the queries' memory is free
+            left -= nt;
+            Cursor next = cur;
+            q_there = false;
+            if (left > 0) {
+                next.next_item(w);
+                if (next.v.qlen * w.group - next.m * BM > h * HALF) {
+                    load_q(next);
+                    q_there = true;
+                }
+            }
+            if (active) {
+                if (!wait(o_done(h, 1), ph ^ 1u)) {            // the last products
                     ok = false;
                     break;
                 }
-                o_ph ^= 1u;
                 tc_fence_after_sync();
                 const float f = whole ? inv_sum(l) : 1.0f;
-                const int64_t at = static_cast<int64_t>(slot) * p.parts.row_cap + r;
+                const int64_t slot_row = static_cast<int64_t>(slot) * p.parts.row_cap;
+                // 128 bytes of each row at a time through the warp's staging
+                // rows, from where eight lanes write a row's 128 bytes
+                const int chunks = whole ? D / 64 : D / 32;
+#pragma unroll 1
+                for (int c = 0; c < chunks; ++c) {
+                    uint32_t x[32];
+                    if (whole) {
+                        uint32_t o[32];
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t o[32];
-                    tmem_ld_32x32b_x32(o_addr + c * 32, o);
-                    tmem_ld_wait();
-                    if (r < rows && whole) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(p.y + row * p.y_stride + hq * D +
-                                                               c * 32);
+                        for (int k = 0; k < 2; ++k) {
+                            tmem_ld_32x32b_x32(o_addr + c * 64 + k * 32, o);
+                            tmem_ld_wait();
+                            loaded32(o);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            uint32_t x[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                x[k] = pack_bf16(__uint_as_float(o[8 * i + 2 * k]) * f,
-                                                 __uint_as_float(o[8 * i + 2 * k + 1]) * f);
-                            dst[i] = make_uint4(x[0], x[1], x[2], x[3]);
+                            for (int i = 0; i < 16; ++i)
+                                x[k * 16 + i] = pack_bf16(__uint_as_float(o[2 * i]) * f,
+                                                          __uint_as_float(o[2 * i + 1]) * f);
                         }
-                    } else if (r < rows) {
-                        uint4 *dst = reinterpret_cast<uint4 *>(p.parts.o + at * D + c * 32);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+                    } else {
+                        tmem_ld_32x32b_x32(o_addr + c * 32, x);
+                        tmem_ld_wait();
+                        loaded32(x);
                     }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         out + lane * 128 + ((i ^ (lane & 7)) << 4)),
+                                     "r"(x[4 * i]), "r"(x[4 * i + 1]), "r"(x[4 * i + 2]),
+                                     "r"(x[4 * i + 3])
+                                     : "memory");
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int at = i * 4 + (lane >> 3);            // row of the warp
+                        uint4 v;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                                     : "r"(out + at * 128 + (((lane & 7) ^ (at & 7)) << 4))
+                                     : "memory");
+                        if (row0 + at < rows) {
+                            void *dst =
+                                whole ? static_cast<void *>(p.y + row_of(cur, row0 + at, p.y_stride) +
+                                                            c * 64)
+                                      : p.parts.o + (slot_row + row0 + at) * D + c * 32;
+                            static_cast<uint4 *>(dst)[lane & 7] = v;
+                        }
+                    }
+                    __syncwarp();
                 }
                 if (r < rows) {
                     if (!whole)
-                        p.parts.ml[at] = make_float2(m, l);
+                        p.parts.ml[slot_row + r] = make_float2(m, l);
                     else if (p.lse != nullptr)
-                        p.lse[row * p.q_heads + hq] = lse_of(m, l);
+                        p.lse[(cur.v.q0 + tok) * static_cast<int64_t>(p.q_heads) +
+                              cur.h * w.group + rr - tok * w.group] = lse_of(m, l);
                 }
             }
-            left -= nt;
-            if (left > 0)
-                cur.next_item(w);
+            cur = next;
         }
         if (!ok)
-            head[0].state = head[1].state = 0;                 // no part that could be merged
+            head[0].rows = head[1].rows = 0;                 // no part that could be merged
     }
     tc_fence_before_sync();
     __syncthreads();
@@ -504,7 +710,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     if (threadIdx.x == 0) {
         if (abort_word)
-            head[0].state = head[1].state = 0;
+            head[0].rows = head[1].rows = 0;
         p.parts.headers[2 * worker] = head[0];
         p.parts.headers[2 * worker + 1] = head[1];
     }

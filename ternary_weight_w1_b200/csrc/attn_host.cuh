@@ -69,6 +69,14 @@ int log2_of(int64_t v)
     return n;
 }
 
+paged::Divide divide_by(int64_t d)
+{
+    if (d == 1)
+        return paged::Divide{0, -1};
+    const int s = log2_of(d);
+    return paged::Divide{static_cast<uint32_t>(((uint64_t(1) << (31 + s)) + d - 1) / d), s - 1};
+}
+
 paged::Seqs device_seqs(const bitlinear_kv_cache &c, const bitlinear_seqs &s, int64_t tokens)
 {
     return paged::Seqs{s.q_start_dev,
@@ -152,11 +160,15 @@ AttnLayout attn_layout(int64_t rows, int64_t head_dim, char *base)
 }
 
 int launch_merge(const attn::Params &p, int64_t head_dim, int workers, int item_rows,
-                 cudaStream_t st)
+                 const DeviceInfo &dev, cudaStream_t st)
 {
     const attn::MergeParams m{p.parts, p.y,    p.y_stride, p.lse,
                               p.q_heads, p.work, workers,    item_rows};
-    const dim3 grid(workers, item_rows / 16), block(attn::MERGE_THREADS);
+    static_assert(kAttnMaxGrid * attn::rows::WARPS <= attn::MERGE_MAX_WORKERS);
+    // a warp a row at most, and a few blocks an SM
+    const int64_t rows = static_cast<int64_t>(p.work.seqs.tokens) * p.q_heads;
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(rows, 4 * dev.sms))),
+        block(attn::MERGE_THREADS);
     return launch_status(head_dim == 64 ? launch(attn::merge_kernel<64>, grid, block, 0, st, m)
                                         : launch(attn::merge_kernel<128>, grid, block, 0, st, m));
 }
@@ -177,7 +189,7 @@ int run_attn_rows(const attn::Params &p, const bitlinear_kv_cache &cache, const 
         e = launch(attn::rows::attn_rows_kernel<D, MT>, dim3(grid), dim3(attn::rows::THREADS),
                    static_cast<size_t>(smem), st, maps, p);
     const int rc = launch_status(e);
-    return rc != BITLINEAR_OK ? rc : launch_merge(p, D, grid * attn::rows::WARPS, 16 * MT, st);
+    return rc != BITLINEAR_OK ? rc : launch_merge(p, D, grid * attn::rows::WARPS, 16 * MT, dev, st);
 }
 
 template <int D>
@@ -196,7 +208,7 @@ int run_attn_chunk(const attn::Params &p, const bitlinear_kv_cache &cache, const
         e = launch(attn::chunk::attn_chunk_kernel<D>, dim3(grid), dim3(attn::chunk::THREADS),
                    static_cast<size_t>(smem), st, maps, p);
     const int rc = launch_status(e);
-    return rc != BITLINEAR_OK ? rc : launch_merge(p, D, grid, attn::chunk::BM, st);
+    return rc != BITLINEAR_OK ? rc : launch_merge(p, D, grid, attn::chunk::BM, dev, st);
 }
 
 // The kernels of a step, by the rows (new tokens times query heads per key
@@ -356,6 +368,7 @@ extern "C" int bitlinear_paged_attention(const void *q_dev, int64_t q_stride, in
     p.work.seqs = device_seqs(*cache, *seqs, tokens);
     p.work.kv_heads = static_cast<int>(cache->kv_heads);
     p.work.group = static_cast<int>(q_heads / cache->kv_heads);
+    p.work.by_group = divide_by(p.work.group);
     p.work.window = static_cast<int>(std::min(window, kAttnMaxKeys));
     const int64_t longest = max_q_len > 0 ? std::min(max_q_len, tokens) : tokens;
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);

@@ -23,6 +23,8 @@
 
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "paged.cuh"
 
@@ -159,27 +161,19 @@ __global__ void __launch_bounds__(THREADS, 1)
             mbar_init(smem_u32(&bars[warp][i]), 1);
         fence_barrier_init();
     }
+    __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
     const paged::Work &w = p.work;
-    paged::group_units<BM, BN>(w, warp, WARPS, sums);
-    __syncthreads();
-    int64_t per_head = 0;
-    for (int g = 0; g < (w.seqs.seqs + 31) / 32; ++g)
-        per_head += sums[g];
-    const int64_t units = per_head * w.kv_heads;
-    const int64_t base = units / workers, extra = units % workers;
-    const int64_t u0 = worker * base + min(static_cast<int64_t>(worker), extra);
-    const int64_t count = base + (worker < extra ? 1 : 0);
+    Cursor cur;
+    const int64_t count = paged::deal<BM, BN>(w, worker, workers, sums, cur);
 
     paged::PartHeader head[2] = {};
     if (count > 0) {
         const int page = 1 << w.seqs.page_shift;
         const int box = min(page, BN);                 // rows of one TMA box
         const int subs = BN / box;                     // boxes of a slice and half
-        Cursor ld, cur;
-        cur.seek(w, sums, per_head, u0);
-        ld = cur;
+        Cursor ld = cur;
 
         // Lane i loads the slice's box i: tensor (k, v), half of the channels,
         // part of the rows. A box without a needed key, or of a page that the
@@ -231,7 +225,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 for (int e = 0; e < 2; ++e) {
                     const int r = mt * 16 + e * 8 + r_lo;
                     const int rr = cur.m * BM + r;
-                    const int tok = rr / w.group;
+                    const int tok = w.by_group(rr);
                     seen_hi[2 * mt + e] = pos0 + tok;
                     const uint32_t *src = reinterpret_cast<const uint32_t *>(
                         p.q + (cur.v.q0 + tok) * p.q_stride +
@@ -259,7 +253,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         o[mt][n][i] = 0.0f;
 
             // keys every row of the item sees: slices inside need no mask
-            const int all_hi = pos0 + (cur.m * BM) / w.group;
+            const int all_hi = pos0 + w.by_group(cur.m * BM);
             const int all_lo = w.window > 0 ? cur.t.khi - w.window : 0;
             for (; done < count; ) {
                 const uint32_t bar = smem_u32(&bars[warp][stage]);
@@ -417,7 +411,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     continue;
                 if (whole) {
                     const int rr = cur.m * BM + r;
-                    const int tok = rr / w.group;
+                    const int tok = w.by_group(rr);
                     const int hq = cur.h * w.group + rr - tok * w.group;
                     const float f = inv_sum(l[i]);
                     uint32_t *dst = reinterpret_cast<uint32_t *>(
@@ -442,7 +436,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             if (!whole)
                 head[from_start ? 1 : 0] =
-                    paged::PartHeader{to_end ? 2 : 1, cur.s, cur.m, cur.h};
+                    paged::PartHeader{rows, to_end ? 0 : 1, cur.v.q0, cur.h + w.kv_heads * cur.m};
             if (done < count)
                 cur.next_item(w);
         }
@@ -455,7 +449,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     parity ^= 1u;
                 }
             }
-            head[0].state = head[1].state = 0;
+            head[0].rows = head[1].rows = 0;
         }
     }
     if (lane < 2)
@@ -466,12 +460,18 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 // ------------------------------------------------------------------- merge
 //
-// Joins the parts of the items that were split between workers, in the order
-// of their keys: o = sum_i 2^(m_i - M) o_i and l likewise, M the largest m_i.
-// Block (x, y) looks at worker x's second slot, where a split item begins, and
-// takes every gridDim.y-th row block of it.
+// Joins the parts of the items that were split between workers: o = sum_i
+// 2^(m_i - M) o_i and l likewise, M the largest m_i. Every block reads all
+// headers, lists the split items, and takes its share of their rows. A warp
+// handles one row, D / 32 channels a lane: its lanes hold the factors of 32
+// parts at a time, and eight parts are in flight together. An item of many
+// parts (a single token behind a long context) spreads the parts of a row over
+// the block's warps, which are then added in a fixed order, so that repeated
+// calls give the same bits.
 
-constexpr int MERGE_THREADS = 128;
+constexpr int MERGE_WARPS = 8;
+constexpr int MERGE_THREADS = MERGE_WARPS * 32;
+constexpr int MERGE_MAX_WORKERS = 1024;
 
 struct MergeParams {
     paged::Parts parts;
@@ -487,66 +487,193 @@ struct MergeParams {
 template <int D>
 __global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const MergeParams p)
 {
-    constexpr int TPR = D / 4;                         // threads per row
-    constexpr int ROWS = MERGE_THREADS / TPR;
+    constexpr int VEC = D / 32;                        // channels of a lane
+    constexpr int PER = MERGE_MAX_WORKERS / MERGE_THREADS;
+    using Vec = typename std::conditional<VEC == 4, float4, float2>::type;
+    __shared__ float partial[MERGE_WARPS][D];
+    __shared__ uint32_t ends[MERGE_MAX_WORKERS / 32];  // first slots that end an item (or hold none)
+    __shared__ int begin[MERGE_MAX_WORKERS + 1];       // first job of the item that starts there
+    __shared__ int16_t count[MERGE_MAX_WORKERS];       // its parts
+    __shared__ paged::PartHeader part[MERGE_MAX_WORKERS];
+    __shared__ int warp_jobs[MERGE_WARPS];
     pdl_wait();
     pdl_launch_dependents();
-    const int first = 2 * blockIdx.x + 1;
-    const paged::PartHeader hd = p.parts.headers[first];
-    if (hd.state != 1)
-        return;
-    // the item goes on in the first slots of the following workers; every warp
-    // looks at 32 of them at a time for the last part
-    int parts = 1;
-    for (int wk = blockIdx.x + 1;; wk += 32) {
-        const int mine = wk + (threadIdx.x & 31);
-        const int state = mine < p.workers ? p.parts.headers[2 * mine].state : 0;
-        const unsigned ends = __ballot_sync(0xffffffffu, state != 1);
-        if (ends == 0) {
-            parts += 32;
-            continue;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // PER consecutive workers a thread
+    const int w0 = threadIdx.x * PER;
+    int rows_of[PER];
+    uint32_t stop = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        rows_of[i] = 0;
+        bool end = true;
+        if (w0 + i < p.workers) {
+            const paged::PartHeader first = p.parts.headers[2 * (w0 + i) + 1];
+            const paged::PartHeader cont = p.parts.headers[2 * (w0 + i)];
+            // a workspace that another call writes at the same time (which is
+            // not allowed) may hold anything: no address comes from it unchecked
+            const int64_t last =
+                static_cast<int64_t>(first.hm / p.work.kv_heads) * p.item_rows + first.rows - 1;
+            if (first.more && first.rows > 0) {
+                if (first.rows <= p.parts.row_cap && first.hm >= 0 && first.row >= 0 &&
+                    last < (int64_t(1) << 31) &&
+                    first.row + static_cast<int64_t>(p.work.by_group(static_cast<int>(last))) <
+                        p.work.seqs.tokens) {
+                    rows_of[i] = first.rows;
+                    part[w0 + i] = first;
+                } else {
+                    paged::fault_index();
+                }
+            }
+            end = cont.rows == 0 || !cont.more;
         }
-        const int at = __ffs(ends) - 1;
-        if (__shfl_sync(0xffffffffu, state, at) != 2)
-            return;                                    // a worker gave up: nothing to join
-        parts += at + 1;
-        break;
+        stop |= (end ? 1u : 0u) << i;
     }
-    const paged::View v = paged::view(p.work.seqs, hd.s);
-    const int group = p.work.group;
-    const int rows = min(p.item_rows, v.qlen * group - hd.m * p.item_rows);
-    const int c = threadIdx.x % TPR;
-    for (int r = blockIdx.y * ROWS + threadIdx.x / TPR; r < rows; r += gridDim.y * ROWS) {
-        auto at = [&](int i) {
-            const int slot = i == 0 ? first : first + 2 * i - 1;
-            return static_cast<int64_t>(slot) * p.parts.row_cap + r;
-        };
-        float top = -INFINITY;
-#pragma unroll 8
-        for (int i = 0; i < parts; ++i)
-            top = fmaxf(top, p.parts.ml[at(i)].x);
-        const float sub = top == -INFINITY ? 0.0f : top;
-        float l = 0.0f;
-        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 8
-        for (int i = 0; i < parts; ++i) {
-            const float2 ml = p.parts.ml[at(i)];
-            const float4 x = *reinterpret_cast<const float4 *>(p.parts.o + at(i) * D + 4 * c);
-            const float f = exp2_approx(ml.x - sub);
-            l = fmaf(ml.y, f, l);
-            o.x = fmaf(x.x, f, o.x);
-            o.y = fmaf(x.y, f, o.y);
-            o.z = fmaf(x.z, f, o.z);
-            o.w = fmaf(x.w, f, o.w);
+    static_assert(PER == 4, "a warp's lanes hold four words' bits of 32 workers");
+    stop <<= 4 * (lane & 7);
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1)
+        stop |= __shfl_xor_sync(0xffffffffu, stop, o);
+    if ((lane & 7) == 0)
+        ends[threadIdx.x >> 3] = stop;
+    __syncthreads();
+    int jobs_of[PER], jobs = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        jobs_of[i] = 0;
+        if (rows_of[i] > 0) {
+            // the next worker behind w0 + i whose first slot ends an item
+            int at = w0 + i + 1;
+            uint32_t bits = at < MERGE_MAX_WORKERS ? ends[at >> 5] >> (at & 31) : 1u;
+            while (bits == 0) {
+                at = (at | 31) + 1;
+                bits = at < MERGE_MAX_WORKERS ? ends[at >> 5] : 1u;
+            }
+            at += __ffs(bits) - 1;
+            const int n = at - (w0 + i) + 1;
+            // an item whose last part is missing (a worker gave up) is left out
+            if (at < p.workers && p.parts.headers[2 * at].rows > 0) {
+                count[w0 + i] = static_cast<int16_t>(n);
+                const int per_pass = n >= 32 ? 1 : n >= 16 ? 2 : n >= 8 ? 4 : 8;
+                jobs_of[i] = (rows_of[i] + per_pass - 1) / per_pass;
+            }
         }
-        const int rr = hd.m * p.item_rows + r;
-        const int tok = rr / group;
-        const int hq = hd.h * group + rr - tok * group;
+        jobs += jobs_of[i];
+    }
+    int upto = jobs;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o)
+            upto += x;
+    }
+    if (lane == 31)
+        warp_jobs[warp] = upto;
+    __syncthreads();
+    int total = 0;
+#pragma unroll
+    for (int k = 0; k < MERGE_WARPS; ++k) {
+        upto += k < warp ? warp_jobs[k] : 0;
+        total += warp_jobs[k];
+    }
+    upto -= jobs;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        begin[w0 + i] = upto;
+        upto += jobs_of[i];
+    }
+    if (threadIdx.x == 0)
+        begin[MERGE_MAX_WORKERS] = total;
+    __syncthreads();
+
+    const int group = p.work.group;
+    const int64_t row_step = p.parts.row_cap;
+    for (int job = blockIdx.x; job < total; job += gridDim.x) {
+        // the last worker whose first job is at most this one
+        int wk = 0;
+#pragma unroll
+        for (int step = MERGE_MAX_WORKERS / 2; step > 0; step >>= 1)
+            if (begin[wk + step] <= job)
+                wk += step;
+        const int first = 2 * wk + 1;
+        const paged::PartHeader hd = part[wk];
+        const int parts = count[wk];
+        // warps a row: as many as leave each at least four parts
+        const int spread = parts >= 32 ? 8 : parts >= 16 ? 4 : parts >= 8 ? 2 : 1;
+        const int sub = warp & (spread - 1);
+        const int r = (job - begin[wk]) * (MERGE_WARPS / spread) + warp / spread;
+        const bool live = r < hd.rows;
+        // part 0 is slot `first`, part i > 0 slot first + 2 i - 1
+        auto at = [&](int i) { return (first + (i > 0 ? 2 * i - 1 : 0)) * row_step + r; };
+        float2 ml = make_float2(-INFINITY, 0.0f);
+        float top = -INFINITY;
+        for (int i = lane; live && i < parts; i += 32) {
+            ml = p.parts.ml[at(i)];
+            top = fmaxf(top, ml.x);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float base = top == -INFINITY ? 0.0f : top;
+        float l = 0.0f;
+        float acc[VEC] = {};
+        for (int i0 = 0; i0 < parts; i0 += 32) {
+            float f = 0.0f;
+            if (live && i0 + lane < parts) {
+                if (parts > 32)
+                    ml = p.parts.ml[at(i0 + lane)];
+                f = exp2_approx(ml.x - base);
+                l = fmaf(ml.y, f, l);
+            }
+            const int n = min(32, parts - i0);
+            for (int b = sub; b < n; b += 8 * spread) {
+                Vec x[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (live && b + k * spread < n)
+                        x[k] = *reinterpret_cast<const Vec *>(
+                            p.parts.o + at(i0 + b + k * spread) * D + VEC * lane);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float g = __shfl_sync(0xffffffffu, f, (b + k * spread) & 31);
+                    if (live && b + k * spread < n) {
+                        const float *e = reinterpret_cast<const float *>(&x[k]);
+#pragma unroll
+                        for (int c = 0; c < VEC; ++c)
+                            acc[c] = fmaf(e[c], g, acc[c]);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            l += __shfl_xor_sync(0xffffffffu, l, o);
+        if (spread > 1) {
+            __syncthreads();                           // the previous job's sums have been read
+#pragma unroll
+            for (int c = 0; c < VEC; ++c)
+                partial[warp][VEC * lane + c] = acc[c];
+            __syncthreads();
+            if (sub == 0)
+                for (int k = 1; k < spread; ++k)
+#pragma unroll
+                    for (int c = 0; c < VEC; ++c)
+                        acc[c] += partial[warp + k][VEC * lane + c];
+        }
+        if (!live || sub != 0)
+            continue;
+        const int m = hd.hm / p.work.kv_heads;
+        const int rr = m * p.item_rows + r;
+        const int tok = p.work.by_group(rr);
+        const int hq = (hd.hm - m * p.work.kv_heads) * group + rr - tok * group;
+        const int64_t row = hd.row + tok;
         const float f = inv_sum(l);
-        *reinterpret_cast<uint2 *>(p.y + (v.q0 + tok) * p.y_stride + hq * D + 4 * c) =
-            make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
-        if (p.lse != nullptr && c == 0)
-            p.lse[static_cast<int64_t>(v.q0 + tok) * p.q_heads + hq] = lse_of(top, l);
+        uint32_t *dst = reinterpret_cast<uint32_t *>(p.y + row * p.y_stride + hq * D + VEC * lane);
+#pragma unroll
+        for (int c = 0; c < VEC / 2; ++c)
+            dst[c] = pack_bf16(acc[2 * c] * f, acc[2 * c + 1] * f);
+        if (p.lse != nullptr && lane == 0)
+            p.lse[row * p.q_heads + hq] = lse_of(top, l);
     }
 }
 

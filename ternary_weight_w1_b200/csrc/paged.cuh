@@ -68,8 +68,22 @@ __device__ __forceinline__ int page_of(const Seqs &q, int s, int c)
 // that gets a whole item writes its output; otherwise it leaves a partial sum
 // that the merge kernel joins in the order of the keys.
 
+// Division of row numbers by a launch constant: n / d for 0 <= n < 2^31 is the
+// high word of n * mul shifted (mul = ceil(2^(31 + s) / d), s = ceil(log2 d):
+// the excess of mul d over 2^(31 + s) is below 2^s, so the quotient is exact).
+struct Divide {
+    uint32_t mul;
+    int shift;             // -1: d is 1
+
+    __device__ __forceinline__ int operator()(int n) const
+    {
+        return shift < 0 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), mul) >> shift);
+    }
+};
+
 struct Work {
     Seqs seqs;
+    Divide by_group;
     int group;             // query heads per key head
     int kv_heads;
     int window;            // 0: none
@@ -87,8 +101,8 @@ template <int BM, int BN>
 __device__ __forceinline__ Tiles item_tiles(const Work &w, const View &v, int m)
 {
     const int r1 = min((m + 1) * BM, v.qlen * w.group) - 1;
-    const int first = v.kv - v.qlen + (m * BM) / w.group;   // position of the first row
-    const int last = v.kv - v.qlen + r1 / w.group;
+    const int first = v.kv - v.qlen + w.by_group(m * BM);   // position of the first row
+    const int last = v.kv - v.qlen + w.by_group(r1);
     Tiles t;
     t.khi = max(last + 1, 0);
     t.klo = w.window > 0 ? max(first - w.window + 1, 0) : 0;
@@ -105,37 +119,62 @@ __device__ __forceinline__ bool in_launch(const Work &w, const View &v)
     return rows >= w.min_rows && rows <= w.max_rows;
 }
 
-template <int BM, int BN>
-__device__ __forceinline__ int64_t seq_units(const Work &w, int s)
+__device__ __forceinline__ int64_t warp_sum(int64_t n)
 {
-    if (s >= w.seqs.seqs)
-        return 0;
-    const View v = view(w.seqs, s);
-    if (!in_launch(w, v))
-        return 0;
-    int64_t n = 0;
-    for (int m = 0; m * BM < v.qlen * w.group; ++m) {
-        const Tiles t = item_tiles<BM, BN>(w, v, m);
-        n += t.end - t.begin;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        n += __shfl_xor_sync(0xffffffffu, n, o);
+    return n;
+}
+
+// sum of the lanes up to this one
+__device__ __forceinline__ int64_t warp_scan(int64_t n)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, n, o);
+        if (lane >= o)
+            n += x;
     }
     return n;
 }
 
-// Units of every group of 32 sequences into sums[] (shared memory). Every warp
-// of the block calls it; a block barrier follows.
+// Units of the 32 sequences of group g, one per lane (the whole warp). A
+// sequence of several items has them counted by all lanes.
 template <int BM, int BN>
-__device__ __forceinline__ void group_units(const Work &w, int warp, int warps, int64_t *sums)
+__device__ __forceinline__ int64_t seq_units(const Work &w, int g)
 {
     const int lane = threadIdx.x & 31;
-    const int groups = (w.seqs.seqs + 31) / 32;
-    for (int g = warp; g < groups; g += warps) {
-        int64_t n = seq_units<BM, BN>(w, g * 32 + lane);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            n += __shfl_xor_sync(0xffffffffu, n, o);
-        if (lane == 0)
-            sums[g] = n;
+    const int s = g * 32 + lane;
+    View v{};
+    if (s < w.seqs.seqs) {
+        v = view(w.seqs, s);
+        if (!in_launch(w, v))
+            v.qlen = 0;
     }
+    const bool many = v.qlen * w.group > BM;
+    int64_t n = 0;
+    if (v.qlen > 0 && !many) {
+        const Tiles t = item_tiles<BM, BN>(w, v, 0);
+        n = t.end - t.begin;
+    }
+    for (unsigned left = __ballot_sync(0xffffffffu, many); left != 0; left &= left - 1) {
+        const int at = __ffs(left) - 1;
+        View x;
+        x.q0 = 0;
+        x.qlen = __shfl_sync(0xffffffffu, v.qlen, at);
+        x.kv = __shfl_sync(0xffffffffu, v.kv, at);
+        int64_t sum = 0;
+        for (int m = lane; m * BM < x.qlen * w.group; m += 32) {
+            const Tiles t = item_tiles<BM, BN>(w, x, m);
+            sum += t.end - t.begin;
+        }
+        sum = warp_sum(sum);
+        if (lane == at)
+            n = sum;
+    }
+    return n;
 }
 
 // A position in the launch's units: the item and the tile inside it.
@@ -168,39 +207,89 @@ struct Cursor {
         open(w);
     }
 
-    // Moves to unit u of a launch of `per_head` units a key head (the whole
-    // warp, with the block's group sums).
-    __device__ __forceinline__ void seek(const Work &w, const int64_t *sums, int64_t per_head,
-                                         int64_t u)
+    // Moves to unit `off` of the 32 sequences of group g, whose units n the
+    // lanes hold (the whole warp).
+    __device__ __forceinline__ void seek(const Work &w, int g, int64_t n, int64_t off)
     {
         const int lane = threadIdx.x & 31;
-        h = static_cast<int>(u / per_head);
-        int64_t off = u - h * per_head;
-        int g = 0;
-        while (off >= sums[g])
-            off -= sums[g++];
-        const int64_t n = seq_units<BM, BN>(w, g * 32 + lane);
-        int64_t upto = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
-            if (lane >= o)
-                upto += x;
-        }
+        const int64_t upto = warp_scan(n);
         const int at = __ffs(__ballot_sync(0xffffffffu, off < upto)) - 1;
         off -= __shfl_sync(0xffffffffu, upto - n, at);
         s = g * 32 + at;
         v = view(w.seqs, s);
         m = 0;
-        open(w);
-        while (off >= t.end - t.begin) {
-            off -= t.end - t.begin;
-            ++m;
-            open(w);
+        // the item, 32 of the sequence's at a time
+        for (int m0 = 0; v.qlen * w.group > BM; m0 += 32) {
+            int64_t k = 0;
+            if ((m0 + lane) * BM < v.qlen * w.group) {
+                const Tiles x = item_tiles<BM, BN>(w, v, m0 + lane);
+                k = x.end - x.begin;
+            }
+            const int64_t sum = warp_scan(k);
+            const unsigned in = __ballot_sync(0xffffffffu, off < sum);
+            if (in != 0) {
+                const int i = __ffs(in) - 1;
+                off -= __shfl_sync(0xffffffffu, sum - k, i);
+                m = m0 + i;
+                break;
+            }
+            off -= __shfl_sync(0xffffffffu, sum, 31);
         }
+        open(w);
         tile = t.begin + static_cast<int>(off);
     }
 };
+
+// n / d where both mostly fit 32 bits, which divide several times faster.
+__device__ __forceinline__ int64_t quotient(int64_t n, int64_t d)
+{
+    return (n | d) >> 31 == 0 ? static_cast<uint32_t>(n) / static_cast<uint32_t>(d) : n / d;
+}
+
+// Deals the launch's units: the number that worker `worker` takes, with `cur`
+// at the first of them. Every warp of the block calls it (`workers` workers in
+// all); `sums` is shared memory for MAX_GROUPS numbers that must not be used
+// for anything else until the block has met again. Up to 32 sequences every
+// warp counts by itself, without a barrier.
+template <int BM, int BN>
+__device__ __forceinline__ int64_t deal(const Work &w, int worker, int workers, int64_t *sums,
+                                        Cursor<BM, BN> &cur)
+{
+    const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int groups = (w.seqs.seqs + 31) / 32;
+    int64_t n = 0, per_head = 0;
+    if (groups == 1) {
+        n = seq_units<BM, BN>(w, 0);
+        per_head = warp_sum(n);
+    } else {
+        for (int g = warp; g < groups; g += warps) {
+            const int64_t x = warp_sum(seq_units<BM, BN>(w, g));
+            if ((threadIdx.x & 31) == 0)
+                sums[g] = x;
+        }
+        __syncthreads();
+        for (int g = threadIdx.x & 31; g < groups; g += 32)
+            per_head += sums[g];
+        per_head = warp_sum(per_head);
+    }
+    const int64_t units = per_head * w.kv_heads;
+    const int64_t base = quotient(units, workers);
+    const int extra = static_cast<int>(units - base * workers);
+    const int64_t count = base + (worker < extra ? 1 : 0);
+    if (count > 0) {
+        const int64_t u = worker * base + min(worker, extra);
+        cur.h = static_cast<int>(quotient(u, per_head));
+        int64_t off = u - cur.h * per_head;
+        int g = 0;
+        if (groups > 1) {
+            while (off >= sums[g])
+                off -= sums[g++];
+            n = seq_units<BM, BN>(w, g);
+        }
+        cur.seek(w, g, n, off);
+    }
+    return count;
+}
 
 // Unnormalised sums of item parts, one slot per end of a worker's run:
 // slot 2w holds the part of an item that began before worker w's run, slot
@@ -208,8 +297,10 @@ struct Cursor {
 // are written by every worker of every launch, so the workspace needs no
 // initialisation.
 struct PartHeader {
-    int state;             // 0: empty, 1: more parts follow, 2: the item's last part
-    int s, m, h;
+    int rows;              // of the item; 0: the slot is empty
+    int more;              // 1: the item goes on in the next worker's first slot
+    int row;               // first query row of the item's sequence
+    int hm;                // key head + kv_heads * item number
 };
 
 struct Parts {

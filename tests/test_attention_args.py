@@ -11,13 +11,25 @@ FAKE = 1 << 20          # a 256-byte-aligned non-null address; never dereference
 BIG = 1 << 40
 
 
+class KVCache(ctypes.Structure):
+    _fields_ = [("k_dev", ctypes.c_void_p), ("v_dev", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("kv_heads", ctypes.c_int64),
+                ("page", ctypes.c_int64), ("head_dim", ctypes.c_int64)]
+
+
+class Seqs(ctypes.Structure):
+    _fields_ = [("q_start_dev", ctypes.c_void_p), ("kv_len_dev", ctypes.c_void_p),
+                ("page_table_dev", ctypes.c_void_p), ("seqs", ctypes.c_int64),
+                ("table_cols", ctypes.c_int64)]
+
+
 def descriptors(kw):
     c = dict(k=FAKE, v=FAKE, pages=10, kv_heads=2, page=16, head_dim=64)
     s = dict(q_start=FAKE, kv_len=FAKE, table=FAKE, seqs=1, cols=4)
     for d in (c, s):
         d.update({n: kw.pop(n) for n in list(kw) if n in d})
-    return (bl._KVCache(c["k"], c["v"], c["pages"], c["kv_heads"], c["page"], c["head_dim"]),
-            bl._Seqs(s["q_start"], s["kv_len"], s["table"], s["seqs"], s["cols"]))
+    return (KVCache(c["k"], c["v"], c["pages"], c["kv_heads"], c["page"], c["head_dim"]),
+            Seqs(s["q_start"], s["kv_len"], s["table"], s["seqs"], s["cols"]))
 
 
 def append(**kw):
