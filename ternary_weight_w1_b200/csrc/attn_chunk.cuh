@@ -1,8 +1,10 @@
 // Attention of many query rows over a paged cache (chunks of prompts and whole
 // prompts) on the fifth-generation tensor cores.
 //
-// An item is 256 rows of one sequence and key head in two halves of 128, each
-// a tcgen05.mma of M = 128. Per step of 64 keys and half h:
+// An item is up to 256 rows of one sequence and key head in two halves of at
+// most 128, as many whole tokens as fit (a token is the group's query heads), so
+// that a half's queries are one box of a tensor map; each half is a tcgen05.mma
+// of M = 128. Per step of 64 keys and half h:
 //   S_h = Q_h K^T          both operands from shared memory, S_h in TMEM
 //   P_h = 2^(scale S_h - m) by four warps, one row per thread, bf16 back into
 //                          the columns of S_h
@@ -16,7 +18,8 @@
 //
 // One persistent block per SM. Warps 0-3 and 4-7 compute the halves' softmax,
 // warp 8 fetches keys and values through a ring of tiles, warps 9 and 10 issue
-// the products of one half each. A warp whose row's maximum has grown rescales its rows of O_h
+// the products of one half each, warp 11 fetches the next item's queries as
+// soon as the last scores of this one are done. A warp whose row's maximum has grown rescales its rows of O_h
 // itself, after the products of the previous step (its o_done).
 #pragma once
 
@@ -26,11 +29,11 @@ namespace bitlinear {
 namespace attn {
 namespace chunk {
 
-constexpr int BM = 256, HALF = 128;    // rows of an item, of a half
+constexpr int HALF = 128;              // most rows of a half item
 constexpr int BN = 128;                // keys of a tile
 constexpr int STEP = 64;               // keys of a step: the tile's two halves
 constexpr int SOFTMAX_WARPS = 8;
-constexpr int THREADS = (SOFTMAX_WARPS + 3) * 32;
+constexpr int THREADS = (SOFTMAX_WARPS + 4) * 32;
 constexpr int TMEM_COLS = 512;
 template <int D>
 struct Cfg {
@@ -171,6 +174,13 @@ __device__ __forceinline__ void exp2_poly2(uint64_t x, float &lo, float &hi)
     hi = __uint_as_float(__float_as_uint(hi) + (__float_as_uint(n1) << 23));
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // 16 columns of the warp's 32 lanes, waited for.
 __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t *r)
 {
@@ -198,13 +208,14 @@ __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t *r)
 
 template <int D>
 __global__ void __launch_bounds__(THREADS, 1)
-    attn_chunk_kernel(const __grid_constant__ Maps maps, const Params p)
+    attn_chunk_kernel(const __grid_constant__ Maps maps, const __grid_constant__ CUtensorMap q_map,
+                      const Params p)
 {
     using C = Cfg<D>;
-    using Cursor = paged::Cursor<BM, BN>;
+    using Cursor = paged::Cursor<BN>;
 
     extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * C::STAGES + 16];
+    __shared__ __align__(8) uint64_t bars[2 * C::STAGES + 18];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_word;
 
@@ -223,16 +234,19 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto s_full = [&](int h, int b) { return bar(2 * C::STAGES + 6 + 2 * h + b); };
     auto p_ready = [&](int h, int b) { return bar(2 * C::STAGES + 10 + 2 * h + b); };
     auto drain_bar = [&](int h) { return bar(2 * C::STAGES + 14 + h); };
+    auto q_free = [&](int h) { return bar(2 * C::STAGES + 16 + h); };
 
     if (threadIdx.x == 0) {
         prefetch_tensormap(&maps.k);
         prefetch_tensormap(&maps.v);
+        prefetch_tensormap(&q_map);
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(full(s), 1);
             mbar_init(empty(s), 2);                            // both halves
         }
         for (int h = 0; h < 2; ++h) {
-            mbar_init(q_ready(h), 4);
+            mbar_init(q_ready(h), 1);
+            mbar_init(q_free(h), 1);
             mbar_init(drain_bar(h), 1);
             for (int b = 0; b < 2; ++b) {
                 mbar_init(o_done(h, b), 1);
@@ -254,7 +268,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const paged::Work &w = p.work;
     const int worker = blockIdx.x;
     Cursor cur;
-    const int64_t count = paged::deal<BM, BN>(w, worker, gridDim.x, sums, cur);
+    const int64_t count = paged::deal<BN>(w, worker, gridDim.x, sums, cur);
     if (w.seqs.seqs > 32)
         __syncthreads();                                       // sums is read; its memory is Q's
 
@@ -271,7 +285,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int64_t n = cur.t.end - cur.tile;
         return static_cast<int>(n < left ? n : left);
     };
-    auto halves_of = [&]() { return cur.v.qlen * w.group - cur.m * BM > HALF ? 2 : 1; };
+    const int half_rows = w.item_rows / 2;                     // whole tokens, at most HALF rows
+    auto rows_of = [&]() { return min(w.item_rows, cur.v.qlen * w.group - cur.m * w.item_rows); };
+    auto halves_of = [&]() { return rows_of() > half_rows ? 2 : 1; };
+
+    // element of channel 0 of row i of cursor c's item in a tensor of rows
+    auto row_of = [&](const Cursor &c, int i, int64_t stride) {
+        const int rr = c.m * w.item_rows + i;
+        const int tok = w.by_group(rr);
+        return (c.v.q0 + tok) * stride + (c.h * w.group + rr - tok * w.group) * D;
+    };
 
     paged::PartHeader head[2] = {};
     int64_t left = count;
@@ -365,6 +388,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     scores(0, k_stage);
                     scores(1, k_stage);
                     umma_commit(empty(k_stage));
+                    if (nt == 1)
+                        umma_commit(q_free(h));
                 }
                 __syncwarp();
                 for (int j = 0; j < nt; ++j) {
@@ -421,6 +446,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                                 scores(b, k_stage);
                                 if (b == 1)
                                     umma_commit(empty(k_stage));
+                                if (b == 1 && j + 2 == nt)
+                                    umma_commit(q_free(h));
                             }
                             __syncwarp();
                         }
@@ -450,63 +477,29 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else if (warp < SOFTMAX_WARPS) {
         // ======================================================== softmax
         const int h = warp >> 2;
-        const int r = h * HALF + (warp & 3) * 32 + lane;       // row of the item
+        const int in_half = (warp & 3) * 32 + lane;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t s_addr = s_tmem(h, 0) + lane_off, o_addr = o_tmem(h) + lane_off;
         const uint32_t out = ring + C::STAGES * C::TILE_BYTES + warp * C::OUT_BYTES;
-        const int row0 = h * HALF + (warp & 3) * 32;           // the warp's first row of the item
         uint32_t ph = 0;                                       // parity of the tile's barriers
-        bool ok = true, q_there = false;
-        // address of channel 0 of item row i of cursor c in a tensor of rows
-        auto row_of = [&](const Cursor &c, int i, int64_t stride) {
-            const int rr = c.m * BM + i;
-            const int tok = w.by_group(rr);
-            return (c.v.q0 + tok) * stride + (c.h * w.group + rr - tok * w.group) * D;
-        };
-        // The warp's 32 rows, D / 8 lanes a row, so that a load covers whole lines.
-        auto load_q = [&](const Cursor &c) {
-            constexpr int PER = D / 8;
-            const int rows = c.v.qlen * w.group - c.m * BM;
-            uint4 x[PER];
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int at = row0 + (i * 32 + lane) / PER;
-                x[i] = at < rows ? __ldg(reinterpret_cast<const uint4 *>(
-                                             p.q + row_of(c, at, p.q_stride)) +
-                                         lane % PER)
-                                 : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int at = row0 - h * HALF + (i * 32 + lane) / PER, ch = lane % PER;
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                 q_smem + h * C::Q_BYTES + (ch >> 3) * (HALF * 128) + at * 128 +
-                                 (((ch & 7) ^ (at & 7)) << 4)),
-                             "r"(x[i].x), "r"(x[i].y), "r"(x[i].z), "r"(x[i].w)
-                             : "memory");
-            }
-            fence_proxy_async();
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(q_ready(h));
-        };
+        bool ok = true;
         while (ok && left > 0) {
             const int nt = parts_tiles(left);
             const bool from_start = cur.tile == cur.t.begin;
             const bool to_end = cur.tile + nt == cur.t.end;
-            const int rows = min(BM, cur.v.qlen * w.group - cur.m * BM);
+            const int rows = rows_of();
             const int slot = 2 * worker + (from_start ? 1 : 0);
             const bool whole = from_start && to_end;
             const bool active = h < halves_of();
             if (!whole)
                 head[from_start ? 1 : 0] = paged::PartHeader{rows, to_end ? 0 : 1, cur.v.q0, cur.h + w.kv_heads * cur.m};
-            const int rr = cur.m * BM + r;
+            // this thread's row of the item, and those of its half
+            const int r = h * half_rows + in_half;
+            const int end = min(rows, (h + 1) * half_rows);
+            const int rr = cur.m * w.item_rows + r;
             const int tok = w.by_group(rr);
             float m = -INFINITY, l = 0.0f;
             if (active) {
-                if (!q_there)
-                    load_q(cur);
                 const int seen_hi = cur.v.kv - cur.v.qlen + tok;     // last key the row sees
                 // keys that every row of this warp sees: tiles inside need no mask
                 const int all_hi = __shfl_sync(0xffffffffu, seen_hi, 0);
@@ -543,9 +536,8 @@ __global__ void __launch_bounds__(THREADS, 1)
                     for (int i = 0; i < STEP; i += 8)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
-                            t4[k] = fmaxf(fmaxf(__uint_as_float(s[i + 2 * k]),
-                                                __uint_as_float(s[i + 2 * k + 1])),
-                                          t4[k]);
+                            t4[k] = max3(__uint_as_float(s[i + 2 * k]),
+                                         __uint_as_float(s[i + 2 * k + 1]), t4[k]);
                     const float top =
                         fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * p.scale_log2;
                     const bool raise = top > m + RESCALE_AT;           // also from -inf
@@ -619,18 +611,6 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
             if (!ok)
                 break;
-            // the next item's queries go ahead of this one's output: its last
-            // scores have been read, so the queries' memory is free
-            left -= nt;
-            Cursor next = cur;
-            q_there = false;
-            if (left > 0) {
-                next.next_item(w);
-                if (next.v.qlen * w.group - next.m * BM > h * HALF) {
-                    load_q(next);
-                    q_there = true;
-                }
-            }
             if (active) {
                 if (!wait(o_done(h, 1), ph ^ 1u)) {            // the last products
                     ok = false;
@@ -639,6 +619,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc_fence_after_sync();
                 const float f = whole ? inv_sum(l) : 1.0f;
                 const int64_t slot_row = static_cast<int64_t>(slot) * p.parts.row_cap;
+                char *dst[8];                                  // of the rows that this lane writes
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int at = r - lane + i * 4 + (lane >> 3);
+                    dst[i] = whole ? reinterpret_cast<char *>(p.y + row_of(cur, at, p.y_stride))
+                                   : reinterpret_cast<char *>(p.parts.o + (slot_row + at) * D);
+                    dst[i] = at < end ? dst[i] + (lane & 7) * 16 : nullptr;
+                }
                 // 128 bytes of each row at a time through the warp's staging
                 // rows, from where eight lanes write a row's 128 bytes
                 const int chunks = whole ? D / 64 : D / 32;
@@ -678,17 +666,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                                      : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                                      : "r"(out + at * 128 + (((lane & 7) ^ (at & 7)) << 4))
                                      : "memory");
-                        if (row0 + at < rows) {
-                            void *dst =
-                                whole ? static_cast<void *>(p.y + row_of(cur, row0 + at, p.y_stride) +
-                                                            c * 64)
-                                      : p.parts.o + (slot_row + row0 + at) * D + c * 32;
-                            static_cast<uint4 *>(dst)[lane & 7] = v;
-                        }
+                        if (dst[i] != nullptr)
+                            *reinterpret_cast<uint4 *>(dst[i] + c * 128) = v;
                     }
                     __syncwarp();
                 }
-                if (r < rows) {
+                if (r < end) {
                     if (!whole)
                         p.parts.ml[slot_row + r] = make_float2(m, l);
                     else if (p.lse != nullptr)
@@ -696,10 +679,48 @@ __global__ void __launch_bounds__(THREADS, 1)
                               cur.h * w.group + rr - tok * w.group] = lse_of(m, l);
                 }
             }
-            cur = next;
+            left -= nt;
+            if (left > 0)
+                cur.next_item(w);
         }
         if (!ok)
             head[0].rows = head[1].rows = 0;                 // no part that could be merged
+    } else {
+        // ======================================================== queries
+        // A box of whole tokens and the group's heads: its rows are the half's.
+        // Rows behind the sequence's last come along (those of other tokens, or
+        // zeros); whatever they hold stays in rows that are never stored.
+        uint32_t ph[2] = {0, 0};
+        int fetched[2] = {0, 0};
+        bool ok = true;
+        while (ok && left > 0) {
+            const int nt = parts_tiles(left);
+            const int tok = cur.v.q0 + w.by_group(cur.m * w.item_rows);
+            for (int h = 0; ok && h < halves_of(); ++h) {
+                ok = wait(q_free(h), ph[h] ^ 1u);
+                if (!ok)
+                    break;
+                ph[h] ^= 1u;
+                fetched[h] = 1;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(q_ready(h), half_rows * D * 2);
+                    for (int c = 0; c < C::CH; ++c)
+                        tma_load_3d(q_smem + h * C::Q_BYTES + c * (HALF * 128), &q_map, c * 64,
+                                    cur.h * w.group, tok + h * w.by_group(half_rows),
+                                    q_ready(h));
+                }
+                __syncwarp();
+            }
+            left -= nt;
+            if (left > 0)
+                cur.next_item(w);
+        }
+        // a block that gave up leaves no copy in flight
+        if (!ok && elect_one())
+            for (int h = 0; h < 2; ++h)
+                if (fetched[h])
+                    drain_wait(q_ready(h), ph[h] ^ 1u, p.wait_limit_ns);
+        __syncwarp();
     }
     tc_fence_before_sync();
     __syncthreads();

@@ -122,6 +122,27 @@ bool make_map_cache(CUtensorMap *map, const void *ptr, const bitlinear_kv_cache 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The queries as a 3-D tensor {head_dim, q_heads, tokens}, boxed as {64
+// channels, the heads of a group, `tokens` tokens}: the rows of half an item.
+bool make_map_q(CUtensorMap *map, const attn::Params &p, int64_t head_dim, int tokens)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr)
+        return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim),
+                                static_cast<cuuint64_t>(p.q_heads),
+                                static_cast<cuuint64_t>(p.work.seqs.tokens)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_dim) * 2,
+                                   static_cast<cuuint64_t>(p.q_stride) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(p.work.group),
+                               static_cast<cuuint32_t>(tokens)};
+    const cuuint32_t estride[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t *>(p.q), dims, strides,
+              box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The parts of one attention kernel inside the workspace: headers, maxima and
 // sums, accumulators, for two slots a worker.
 size_t parts_layout(int64_t workers, int64_t row_cap, int64_t head_dim, char *base,
@@ -154,30 +175,30 @@ AttnLayout attn_layout(int64_t rows, int64_t head_dim, char *base)
     l.bytes = parts_layout(kAttnMaxGrid * attn::rows::WARPS, std::min<int64_t>(rows, kRowsKernelMax),
                            head_dim, base, &l.rows);
     if (rows > kRowsKernelMax)
-        l.bytes += parts_layout(kAttnMaxGrid, std::min<int64_t>(rows, attn::chunk::BM), head_dim,
+        l.bytes += parts_layout(kAttnMaxGrid, std::min<int64_t>(rows, 2 * attn::chunk::HALF), head_dim,
                                 base + l.bytes, &l.chunk);
     return l;
 }
 
-int launch_merge(const attn::Params &p, int64_t head_dim, int workers, int item_rows,
-                 const DeviceInfo &dev, cudaStream_t st)
+int launch_merge(const attn::Params &p, int64_t head_dim, int workers, const DeviceInfo &dev,
+                 cudaStream_t st)
 {
-    const attn::MergeParams m{p.parts, p.y,    p.y_stride, p.lse,
-                              p.q_heads, p.work, workers,    item_rows};
+    const attn::MergeParams m{p.parts, p.y, p.y_stride, p.lse, p.q_heads, p.work, workers};
     static_assert(kAttnMaxGrid * attn::rows::WARPS <= attn::MERGE_MAX_WORKERS);
-    // a warp a row at most, and a few blocks an SM
+    // one wave at most, and no more blocks than there are rows
     const int64_t rows = static_cast<int64_t>(p.work.seqs.tokens) * p.q_heads;
-    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(rows, 4 * dev.sms))),
+    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(rows, dev.sms))),
         block(attn::MERGE_THREADS);
     return launch_status(head_dim == 64 ? launch(attn::merge_kernel<64>, grid, block, 0, st, m)
                                         : launch(attn::merge_kernel<128>, grid, block, 0, st, m));
 }
 
 template <int D, int MT>
-int run_attn_rows(const attn::Params &p, const bitlinear_kv_cache &cache, const DeviceInfo &dev,
+int run_attn_rows(attn::Params p, const bitlinear_kv_cache &cache, const DeviceInfo &dev,
                   cudaStream_t st)
 {
     constexpr int smem = attn::rows::Cfg<D>::SMEM_BYTES;
+    p.work.item_rows = 16 * MT;
     attn::Maps maps{};
     const uint32_t box = static_cast<uint32_t>(std::min<int64_t>(cache.page, attn::rows::BN));
     if (!make_map_cache(&maps.k, cache.k_dev, cache, box) ||
@@ -189,15 +210,20 @@ int run_attn_rows(const attn::Params &p, const bitlinear_kv_cache &cache, const 
         e = launch(attn::rows::attn_rows_kernel<D, MT>, dim3(grid), dim3(attn::rows::THREADS),
                    static_cast<size_t>(smem), st, maps, p);
     const int rc = launch_status(e);
-    return rc != BITLINEAR_OK ? rc : launch_merge(p, D, grid * attn::rows::WARPS, 16 * MT, dev, st);
+    return rc != BITLINEAR_OK ? rc : launch_merge(p, D, grid * attn::rows::WARPS, dev, st);
 }
 
 template <int D>
-int run_attn_chunk(const attn::Params &p, const bitlinear_kv_cache &cache, const DeviceInfo &dev,
+int run_attn_chunk(attn::Params p, const bitlinear_kv_cache &cache, const DeviceInfo &dev,
                    cudaStream_t st)
 {
     constexpr int smem = attn::chunk::Cfg<D>::SMEM_BYTES;
+    const int tokens = attn::chunk::HALF / p.work.group;       // of half an item
+    p.work.item_rows = 2 * tokens * p.work.group;
     attn::Maps maps{};
+    CUtensorMap q_map;
+    if (!make_map_q(&q_map, p, D, tokens))
+        return BITLINEAR_ERR_CUDA;
     const uint32_t box = static_cast<uint32_t>(std::min<int64_t>(cache.page, attn::chunk::BN));
     if (!make_map_cache(&maps.k, cache.k_dev, cache, box) ||
         !make_map_cache(&maps.v, cache.v_dev, cache, box))
@@ -206,9 +232,9 @@ int run_attn_chunk(const attn::Params &p, const bitlinear_kv_cache &cache, const
     cudaError_t e = allow_smem<attn::chunk::attn_chunk_kernel<D>>(dev.id, smem);
     if (e == cudaSuccess)
         e = launch(attn::chunk::attn_chunk_kernel<D>, dim3(grid), dim3(attn::chunk::THREADS),
-                   static_cast<size_t>(smem), st, maps, p);
+                   static_cast<size_t>(smem), st, maps, q_map, p);
     const int rc = launch_status(e);
-    return rc != BITLINEAR_OK ? rc : launch_merge(p, D, grid, attn::chunk::BM, dev, st);
+    return rc != BITLINEAR_OK ? rc : launch_merge(p, D, grid, dev, st);
 }
 
 // The kernels of a step, by the rows (new tokens times query heads per key
@@ -229,7 +255,7 @@ int run_attention(attn::Params p, const bitlinear_kv_cache &cache, int64_t max_r
     p.parts = layout.rows;
     if (max_rows <= 16)
         return run_attn_rows<D, 1>(p, cache, dev, st);
-    if (max_rows <= kRowsKernelMax)
+    if (max_rows <= kRowsKernelMax || p.work.group > attn::chunk::HALF)
         return run_attn_rows<D, 2>(p, cache, dev, st);
     if (rows < 64 * static_cast<int64_t>(p.work.seqs.seqs)) {
         const bool small = p.work.group <= 16;

@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr int BM = 16 * MT;
     constexpr int KS = D / 16;             // k-steps of the score product
     constexpr int NT = D / 8;              // 8-channel tiles of the output
-    using Cursor = paged::Cursor<BM, BN>;
+    using Cursor = paged::Cursor<BN>;
 
     extern __shared__ uint8_t smem_raw[];
     __shared__ int64_t sums[paged::MAX_GROUPS];
@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     pdl_launch_dependents();
     const paged::Work &w = p.work;
     Cursor cur;
-    const int64_t count = paged::deal<BM, BN>(w, worker, workers, sums, cur);
+    const int64_t count = paged::deal<BN>(w, worker, workers, sums, cur);
 
     paged::PartHeader head[2] = {};
     if (count > 0) {
@@ -462,16 +462,25 @@ __global__ void __launch_bounds__(THREADS, 1)
 //
 // Joins the parts of the items that were split between workers: o = sum_i
 // 2^(m_i - M) o_i and l likewise, M the largest m_i. Every block reads all
-// headers, lists the split items, and takes its share of their rows. A warp
-// handles one row, D / 32 channels a lane: its lanes hold the factors of 32
-// parts at a time, and eight parts are in flight together. An item of many
-// parts (a single token behind a long context) spreads the parts of a row over
-// the block's warps, which are then added in a fixed order, so that repeated
-// calls give the same bits.
+// headers, lists the split items (each begins in some worker's second slot),
+// and takes its share of the jobs, groups of their rows: one wave of blocks
+// whatever the items are. (A block per worker and row group spent 15 us on
+// launching blocks that found nothing.) A warp's lanes take D / 32 channels
+// each of a row and have eight parts in flight: of one row, or of two or four
+// rows when the item has few parts. With many parts (a single token behind a long
+// context) the parts of a row are spread over the block's warps, which are then
+// added in a fixed order, so that repeated calls give the same bits.
 
 constexpr int MERGE_WARPS = 8;
 constexpr int MERGE_THREADS = MERGE_WARPS * 32;
 constexpr int MERGE_MAX_WORKERS = 1024;
+
+// Rows that a block joins at a time, by the item's parts: see few() and the
+// spread below.
+__device__ __forceinline__ int merge_job_rows(int parts)
+{
+    return parts <= 2 ? 32 : parts <= 4 ? 16 : parts <= 8 ? 8 : parts < 16 ? 4 : parts < 32 ? 2 : 1;
+}
 
 struct MergeParams {
     paged::Parts parts;
@@ -481,67 +490,141 @@ struct MergeParams {
     int q_heads;
     paged::Work work;
     int workers;
-    int item_rows;             // BM of the kernel that left the parts
+};
+
+template <int D>
+struct Merge {
+    static constexpr int VEC = D / 32;                 // channels of a lane
+    using Vec = typename std::conditional<VEC == 4, float4, float2>::type;
+
+    const MergeParams &p;
+    paged::PartHeader hd;
+    int first, parts, lane, m;
+
+    // part 0 is slot `first`, part i > 0 slot first + 2 i - 1
+    __device__ __forceinline__ int64_t at(int i, int r) const
+    {
+        return static_cast<int64_t>(first + (i > 0 ? 2 * i - 1 : 0)) * p.parts.row_cap + r;
+    }
+
+    __device__ __forceinline__ Vec load(int i, int r) const
+    {
+        return *reinterpret_cast<const Vec *>(p.parts.o + at(i, r) * D + VEC * lane);
+    }
+
+    static __device__ __forceinline__ void add(float (&acc)[VEC], const Vec &x, float f)
+    {
+        const float *e = reinterpret_cast<const float *>(&x);
+#pragma unroll
+        for (int c = 0; c < VEC; ++c)
+            acc[c] = fmaf(e[c], f, acc[c]);
+    }
+
+    __device__ __forceinline__ void store(int r, const float (&acc)[VEC], float top, float l) const
+    {
+        const int rr = m * p.work.item_rows + r;
+        const int tok = p.work.by_group(rr);
+        const int hq = (hd.hm - m * p.work.kv_heads) * p.work.group + rr - tok * p.work.group;
+        const int64_t row = hd.row + tok;
+        const float f = inv_sum(l);
+        uint32_t *dst = reinterpret_cast<uint32_t *>(p.y + row * p.y_stride + hq * D + VEC * lane);
+#pragma unroll
+        for (int c = 0; c < VEC / 2; ++c)
+            dst[c] = pack_bf16(acc[2 * c] * f, acc[2 * c + 1] * f);
+        if (p.lse != nullptr && lane == 0)
+            p.lse[row * p.q_heads + hq] = lse_of(top, l);
+    }
+
+    // Rows r .. r + 8 / NP of an item of at most NP parts: lane 8 i + j holds
+    // part j of row i.
+    template <int NP>
+    __device__ __forceinline__ void few(int r) const
+    {
+        constexpr int ROWS = 8 / NP;
+        const int i = lane >> 3, j = lane & 7;
+        float2 ml = make_float2(-INFINITY, 0.0f);
+        if (i < ROWS && j < parts && r + i < hd.rows)
+            ml = p.parts.ml[at(j, r + i)];
+        Vec x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (k % NP < parts && r + k / NP < hd.rows)
+                x[k] = load(k % NP, r + k / NP);
+        float top = ml.x;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float f = exp2_approx(ml.x - (top == -INFINITY ? 0.0f : top));
+        float l = ml.y * f;
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1)
+            l += __shfl_xor_sync(0xffffffffu, l, o);
+#pragma unroll
+        for (int q = 0; q < ROWS; ++q) {
+            float acc[VEC] = {};
+#pragma unroll
+            for (int k = 0; k < NP; ++k) {
+                const float g = __shfl_sync(0xffffffffu, f, 8 * q + k);
+                if (k < parts && r + q < hd.rows)
+                    add(acc, x[q * NP + k], g);
+            }
+            const float t = __shfl_sync(0xffffffffu, top, 8 * q);
+            const float s = __shfl_sync(0xffffffffu, l, 8 * q);
+            if (r + q < hd.rows)
+                store(r + q, acc, t, s);
+        }
+    }
 };
 
 template <int D>
 __global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const MergeParams p)
 {
-    constexpr int VEC = D / 32;                        // channels of a lane
+    using M = Merge<D>;
     constexpr int PER = MERGE_MAX_WORKERS / MERGE_THREADS;
-    using Vec = typename std::conditional<VEC == 4, float4, float2>::type;
     __shared__ float partial[MERGE_WARPS][D];
     __shared__ uint32_t ends[MERGE_MAX_WORKERS / 32];  // first slots that end an item (or hold none)
-    __shared__ int begin[MERGE_MAX_WORKERS + 1];       // first job of the item that starts there
+    __shared__ int begin[MERGE_MAX_WORKERS];           // first job of the item that starts there
     __shared__ int16_t count[MERGE_MAX_WORKERS];       // its parts
-    __shared__ paged::PartHeader part[MERGE_MAX_WORKERS];
+    __shared__ uint32_t empty[MERGE_MAX_WORKERS / 32]; // first slots that hold none
     __shared__ int warp_jobs[MERGE_WARPS];
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // PER consecutive workers a thread
     const int w0 = threadIdx.x * PER;
-    int rows_of[PER];
-    uint32_t stop = 0;
+    int2 cont[PER], start[PER];                        // {rows, more} of the workers' two slots
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        rows_of[i] = 0;
-        bool end = true;
+        cont[i] = start[i] = make_int2(0, 0);
         if (w0 + i < p.workers) {
-            const paged::PartHeader first = p.parts.headers[2 * (w0 + i) + 1];
-            const paged::PartHeader cont = p.parts.headers[2 * (w0 + i)];
-            // a workspace that another call writes at the same time (which is
-            // not allowed) may hold anything: no address comes from it unchecked
-            const int64_t last =
-                static_cast<int64_t>(first.hm / p.work.kv_heads) * p.item_rows + first.rows - 1;
-            if (first.more && first.rows > 0) {
-                if (first.rows <= p.parts.row_cap && first.hm >= 0 && first.row >= 0 &&
-                    last < (int64_t(1) << 31) &&
-                    first.row + static_cast<int64_t>(p.work.by_group(static_cast<int>(last))) <
-                        p.work.seqs.tokens) {
-                    rows_of[i] = first.rows;
-                    part[w0 + i] = first;
-                } else {
-                    paged::fault_index();
-                }
-            }
-            end = cont.rows == 0 || !cont.more;
+            cont[i] = *reinterpret_cast<const int2 *>(p.parts.headers + 2 * (w0 + i));
+            start[i] = *reinterpret_cast<const int2 *>(p.parts.headers + 2 * (w0 + i) + 1);
         }
-        stop |= (end ? 1u : 0u) << i;
+    }
+    uint32_t stop = 0, none = 0;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        stop |= (cont[i].x == 0 || cont[i].y == 0 ? 1u : 0u) << i;
+        none |= (cont[i].x == 0 ? 1u : 0u) << i;
     }
     static_assert(PER == 4, "a warp's lanes hold four words' bits of 32 workers");
     stop <<= 4 * (lane & 7);
+    none <<= 4 * (lane & 7);
 #pragma unroll
-    for (int o = 1; o < 8; o <<= 1)
+    for (int o = 1; o < 8; o <<= 1) {
         stop |= __shfl_xor_sync(0xffffffffu, stop, o);
-    if ((lane & 7) == 0)
+        none |= __shfl_xor_sync(0xffffffffu, none, o);
+    }
+    if ((lane & 7) == 0) {
         ends[threadIdx.x >> 3] = stop;
+        empty[threadIdx.x >> 3] = none;
+    }
     __syncthreads();
     int jobs_of[PER], jobs = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         jobs_of[i] = 0;
-        if (rows_of[i] > 0) {
+        if (start[i].x > 0 && start[i].x <= p.parts.row_cap && start[i].y != 0) {
             // the next worker behind w0 + i whose first slot ends an item
             int at = w0 + i + 1;
             uint32_t bits = at < MERGE_MAX_WORKERS ? ends[at >> 5] >> (at & 31) : 1u;
@@ -550,12 +633,12 @@ __global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const MergeParams 
                 bits = at < MERGE_MAX_WORKERS ? ends[at >> 5] : 1u;
             }
             at += __ffs(bits) - 1;
-            const int n = at - (w0 + i) + 1;
-            // an item whose last part is missing (a worker gave up) is left out
-            if (at < p.workers && p.parts.headers[2 * at].rows > 0) {
+            // (an item whose last part is missing, as a worker gave up, is left out)
+            if (at < MERGE_MAX_WORKERS && ((empty[at >> 5] >> (at & 31)) & 1u) == 0) {
+                const int n = at - (w0 + i) + 1;
                 count[w0 + i] = static_cast<int16_t>(n);
-                const int per_pass = n >= 32 ? 1 : n >= 16 ? 2 : n >= 8 ? 4 : 8;
-                jobs_of[i] = (rows_of[i] + per_pass - 1) / per_pass;
+                const int job = merge_job_rows(n);
+                jobs_of[i] = (start[i].x + job - 1) / job;
             }
         }
         jobs += jobs_of[i];
@@ -582,12 +665,8 @@ __global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const MergeParams 
         begin[w0 + i] = upto;
         upto += jobs_of[i];
     }
-    if (threadIdx.x == 0)
-        begin[MERGE_MAX_WORKERS] = total;
     __syncthreads();
 
-    const int group = p.work.group;
-    const int64_t row_step = p.parts.row_cap;
     for (int job = blockIdx.x; job < total; job += gridDim.x) {
         // the last worker whose first job is at most this one
         int wk = 0;
@@ -595,20 +674,38 @@ __global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const MergeParams 
         for (int step = MERGE_MAX_WORKERS / 2; step > 0; step >>= 1)
             if (begin[wk + step] <= job)
                 wk += step;
-        const int first = 2 * wk + 1;
-        const paged::PartHeader hd = part[wk];
-        const int parts = count[wk];
-        // warps a row: as many as leave each at least four parts
-        const int spread = parts >= 32 ? 8 : parts >= 16 ? 4 : parts >= 8 ? 2 : 1;
+        M mg{p, p.parts.headers[2 * wk + 1], 2 * wk + 1, count[wk], lane, 0};
+        mg.m = mg.hd.hm / p.work.kv_heads;
+        const int rows = mg.hd.rows, parts = mg.parts;
+        // a workspace that another call writes at the same time (which is not
+        // allowed) may hold anything: no address comes from it unchecked
+        const int64_t last = static_cast<int64_t>(mg.m) * p.work.item_rows + rows - 1;
+        if (rows < 0 || rows > p.parts.row_cap || mg.hd.hm < 0 || mg.hd.row < 0 ||
+            last >= (int64_t(1) << 31) ||
+            mg.hd.row + static_cast<int64_t>(p.work.by_group(static_cast<int>(last))) >=
+                p.work.seqs.tokens) {
+            paged::fault_index();
+            return;
+        }
+        const int r0 = (job - begin[wk]) * merge_job_rows(parts);
+        if (parts <= 8) {
+            if (parts <= 2)
+                mg.template few<2>(r0 + 4 * warp);
+            else if (parts <= 4)
+                mg.template few<4>(r0 + 2 * warp);
+            else
+                mg.template few<8>(r0 + warp);
+            continue;
+        }
+        // warps a row: as many as leave each about four parts
+        const int spread = parts >= 32 ? 8 : parts >= 16 ? 4 : 2;
         const int sub = warp & (spread - 1);
-        const int r = (job - begin[wk]) * (MERGE_WARPS / spread) + warp / spread;
-        const bool live = r < hd.rows;
-        // part 0 is slot `first`, part i > 0 slot first + 2 i - 1
-        auto at = [&](int i) { return (first + (i > 0 ? 2 * i - 1 : 0)) * row_step + r; };
+        const int r = r0 + warp / spread;
+        const bool live = r < rows;
         float2 ml = make_float2(-INFINITY, 0.0f);
         float top = -INFINITY;
         for (int i = lane; live && i < parts; i += 32) {
-            ml = p.parts.ml[at(i)];
+            ml = p.parts.ml[mg.at(i, r)];
             top = fmaxf(top, ml.x);
         }
 #pragma unroll
@@ -616,64 +713,45 @@ __global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const MergeParams 
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float base = top == -INFINITY ? 0.0f : top;
         float l = 0.0f;
-        float acc[VEC] = {};
+        float acc[M::VEC] = {};
         for (int i0 = 0; i0 < parts; i0 += 32) {
             float f = 0.0f;
             if (live && i0 + lane < parts) {
                 if (parts > 32)
-                    ml = p.parts.ml[at(i0 + lane)];
+                    ml = p.parts.ml[mg.at(i0 + lane, r)];
                 f = exp2_approx(ml.x - base);
                 l = fmaf(ml.y, f, l);
             }
             const int n = min(32, parts - i0);
             for (int b = sub; b < n; b += 8 * spread) {
-                Vec x[8];
+                typename M::Vec x[8];
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     if (live && b + k * spread < n)
-                        x[k] = *reinterpret_cast<const Vec *>(
-                            p.parts.o + at(i0 + b + k * spread) * D + VEC * lane);
+                        x[k] = mg.load(i0 + b + k * spread, r);
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
                     const float g = __shfl_sync(0xffffffffu, f, (b + k * spread) & 31);
-                    if (live && b + k * spread < n) {
-                        const float *e = reinterpret_cast<const float *>(&x[k]);
-#pragma unroll
-                        for (int c = 0; c < VEC; ++c)
-                            acc[c] = fmaf(e[c], g, acc[c]);
-                    }
+                    if (live && b + k * spread < n)
+                        M::add(acc, x[k], g);
                 }
             }
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             l += __shfl_xor_sync(0xffffffffu, l, o);
-        if (spread > 1) {
-            __syncthreads();                           // the previous job's sums have been read
+        __syncthreads();                               // the previous job's sums have been read
 #pragma unroll
-            for (int c = 0; c < VEC; ++c)
-                partial[warp][VEC * lane + c] = acc[c];
-            __syncthreads();
-            if (sub == 0)
-                for (int k = 1; k < spread; ++k)
+        for (int c = 0; c < M::VEC; ++c)
+            partial[warp][M::VEC * lane + c] = acc[c];
+        __syncthreads();
+        if (live && sub == 0) {
+            for (int k = 1; k < spread; ++k)
 #pragma unroll
-                    for (int c = 0; c < VEC; ++c)
-                        acc[c] += partial[warp + k][VEC * lane + c];
+                for (int c = 0; c < M::VEC; ++c)
+                    acc[c] += partial[warp + k][M::VEC * lane + c];
+            mg.store(r, acc, top, l);
         }
-        if (!live || sub != 0)
-            continue;
-        const int m = hd.hm / p.work.kv_heads;
-        const int rr = m * p.item_rows + r;
-        const int tok = p.work.by_group(rr);
-        const int hq = (hd.hm - m * p.work.kv_heads) * group + rr - tok * group;
-        const int64_t row = hd.row + tok;
-        const float f = inv_sum(l);
-        uint32_t *dst = reinterpret_cast<uint32_t *>(p.y + row * p.y_stride + hq * D + VEC * lane);
-#pragma unroll
-        for (int c = 0; c < VEC / 2; ++c)
-            dst[c] = pack_bf16(acc[2 * c] * f, acc[2 * c + 1] * f);
-        if (p.lse != nullptr && lane == 0)
-            p.lse[row * p.q_heads + hq] = lse_of(top, l);
     }
 }
 

@@ -58,8 +58,8 @@ __device__ __forceinline__ int page_of(const Seqs &q, int s, int c)
 
 // ---------------------------------------------------------------- schedule
 //
-// The attention's work is cut into items: BM consecutive rows of one sequence
-// and key head, where row r is query head r % group of token r / group, so the
+// The attention's work is cut into items: item_rows consecutive rows of one
+// sequence and key head, where row r is query head r % group of token r / group, so the
 // query heads that share a key head share its tiles. An item takes one unit
 // per tile of BN keys that any of its rows sees. All units of a launch, items
 // in order and key heads outermost, are dealt to the workers in equal
@@ -86,6 +86,7 @@ struct Work {
     Divide by_group;
     int group;             // query heads per key head
     int kv_heads;
+    int item_rows;         // rows of an item
     int window;            // 0: none
     int min_rows, max_rows;  // sequences of this launch: min_rows <= qlen * group <= max_rows
 };
@@ -97,11 +98,23 @@ struct Tiles {
     int klo, khi;          // keys that any row of the item sees
 };
 
-template <int BM, int BN>
+// The k-th item of a sequence of n: the rows nearest its end, which see the most
+// keys, take turns with those nearest its beginning, so that a run of units
+// never holds many short items.
+__device__ __forceinline__ int item_at(int k, int n) { return (k & 1) ? k >> 1 : n - 1 - (k >> 1); }
+
+__device__ __forceinline__ int items_of(const Work &w, const View &v)
+{
+    return static_cast<int>(static_cast<unsigned>(v.qlen * w.group + w.item_rows - 1) /
+                            static_cast<unsigned>(w.item_rows));
+}
+
+// Key tiles of rows m * item_rows .. of a sequence.
+template <int BN>
 __device__ __forceinline__ Tiles item_tiles(const Work &w, const View &v, int m)
 {
-    const int r1 = min((m + 1) * BM, v.qlen * w.group) - 1;
-    const int first = v.kv - v.qlen + w.by_group(m * BM);   // position of the first row
+    const int r1 = min((m + 1) * w.item_rows, v.qlen * w.group) - 1;
+    const int first = v.kv - v.qlen + w.by_group(m * w.item_rows);   // position of the first row
     const int last = v.kv - v.qlen + w.by_group(r1);
     Tiles t;
     t.khi = max(last + 1, 0);
@@ -142,7 +155,7 @@ __device__ __forceinline__ int64_t warp_scan(int64_t n)
 
 // Units of the 32 sequences of group g, one per lane (the whole warp). A
 // sequence of several items has them counted by all lanes.
-template <int BM, int BN>
+template <int BN>
 __device__ __forceinline__ int64_t seq_units(const Work &w, int g)
 {
     const int lane = threadIdx.x & 31;
@@ -153,10 +166,10 @@ __device__ __forceinline__ int64_t seq_units(const Work &w, int g)
         if (!in_launch(w, v))
             v.qlen = 0;
     }
-    const bool many = v.qlen * w.group > BM;
+    const bool many = v.qlen * w.group > w.item_rows;
     int64_t n = 0;
     if (v.qlen > 0 && !many) {
-        const Tiles t = item_tiles<BM, BN>(w, v, 0);
+        const Tiles t = item_tiles<BN>(w, v, 0);
         n = t.end - t.begin;
     }
     for (unsigned left = __ballot_sync(0xffffffffu, many); left != 0; left &= left - 1) {
@@ -166,8 +179,8 @@ __device__ __forceinline__ int64_t seq_units(const Work &w, int g)
         x.qlen = __shfl_sync(0xffffffffu, v.qlen, at);
         x.kv = __shfl_sync(0xffffffffu, v.kv, at);
         int64_t sum = 0;
-        for (int m = lane; m * BM < x.qlen * w.group; m += 32) {
-            const Tiles t = item_tiles<BM, BN>(w, x, m);
+        for (int m = lane; m * w.item_rows < x.qlen * w.group; m += 32) {
+            const Tiles t = item_tiles<BN>(w, x, m);
             sum += t.end - t.begin;
         }
         sum = warp_sum(sum);
@@ -178,15 +191,16 @@ __device__ __forceinline__ int64_t seq_units(const Work &w, int g)
 }
 
 // A position in the launch's units: the item and the tile inside it.
-template <int BM, int BN>
+template <int BN>
 struct Cursor {
-    int h, s, m, tile;
+    int h, s, k, m, tile;  // k-th item of the sequence: rows m * w.item_rows ..
     View v;
     Tiles t;
 
     __device__ __forceinline__ void open(const Work &w)
     {
-        t = item_tiles<BM, BN>(w, v, m);
+        m = item_at(k, items_of(w, v));
+        t = item_tiles<BN>(w, v, m);
         tile = t.begin;
     }
 
@@ -194,8 +208,8 @@ struct Cursor {
     // sequence of this launch is always found.
     __device__ __forceinline__ void next_item(const Work &w)
     {
-        if (++m * BM >= v.qlen * w.group) {
-            m = 0;
+        if (++k * w.item_rows >= v.qlen * w.group) {
+            k = 0;
             do {
                 if (++s == w.seqs.seqs) {
                     s = 0;
@@ -217,20 +231,21 @@ struct Cursor {
         off -= __shfl_sync(0xffffffffu, upto - n, at);
         s = g * 32 + at;
         v = view(w.seqs, s);
-        m = 0;
+        k = 0;
         // the item, 32 of the sequence's at a time
-        for (int m0 = 0; v.qlen * w.group > BM; m0 += 32) {
-            int64_t k = 0;
-            if ((m0 + lane) * BM < v.qlen * w.group) {
-                const Tiles x = item_tiles<BM, BN>(w, v, m0 + lane);
-                k = x.end - x.begin;
+        const int items = items_of(w, v);
+        for (int k0 = 0; items > 1; k0 += 32) {
+            int64_t c = 0;
+            if (k0 + lane < items) {
+                const Tiles x = item_tiles<BN>(w, v, item_at(k0 + lane, items));
+                c = x.end - x.begin;
             }
-            const int64_t sum = warp_scan(k);
+            const int64_t sum = warp_scan(c);
             const unsigned in = __ballot_sync(0xffffffffu, off < sum);
             if (in != 0) {
                 const int i = __ffs(in) - 1;
-                off -= __shfl_sync(0xffffffffu, sum - k, i);
-                m = m0 + i;
+                off -= __shfl_sync(0xffffffffu, sum - c, i);
+                k = k0 + i;
                 break;
             }
             off -= __shfl_sync(0xffffffffu, sum, 31);
@@ -251,19 +266,19 @@ __device__ __forceinline__ int64_t quotient(int64_t n, int64_t d)
 // all); `sums` is shared memory for MAX_GROUPS numbers that must not be used
 // for anything else until the block has met again. Up to 32 sequences every
 // warp counts by itself, without a barrier.
-template <int BM, int BN>
+template <int BN>
 __device__ __forceinline__ int64_t deal(const Work &w, int worker, int workers, int64_t *sums,
-                                        Cursor<BM, BN> &cur)
+                                        Cursor<BN> &cur)
 {
     const int warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int groups = (w.seqs.seqs + 31) / 32;
     int64_t n = 0, per_head = 0;
     if (groups == 1) {
-        n = seq_units<BM, BN>(w, 0);
+        n = seq_units<BN>(w, 0);
         per_head = warp_sum(n);
     } else {
         for (int g = warp; g < groups; g += warps) {
-            const int64_t x = warp_sum(seq_units<BM, BN>(w, g));
+            const int64_t x = warp_sum(seq_units<BN>(w, g));
             if ((threadIdx.x & 31) == 0)
                 sums[g] = x;
         }
@@ -284,7 +299,7 @@ __device__ __forceinline__ int64_t deal(const Work &w, int worker, int workers, 
         if (groups > 1) {
             while (off >= sums[g])
                 off -= sums[g++];
-            n = seq_units<BM, BN>(w, g);
+            n = seq_units<BN>(w, g);
         }
         cur.seek(w, g, n, off);
     }
