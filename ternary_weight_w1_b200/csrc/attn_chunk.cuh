@@ -6,8 +6,7 @@
 // that a half's queries are one box of a tensor map; each half is a tcgen05.mma
 // of M = 128. Per step of 64 keys and half h:
 //   S_h = Q_h K^T          both operands from shared memory, S_h in TMEM
-//   P_h = 2^(scale S_h - m) by four warps, one row per thread, bf16 back into
-//                          the columns of S_h
+//   P_h = 2^(scale S_h - m) by eight warps, bf16 back into the columns of S_h
 //   O_h += P_h V           P_h from TMEM, V from shared memory as it lies there
 //                          (its channels contiguous: an MN-major operand)
 // Each half has two S buffers, which the two steps of a 128-key tile take in
@@ -16,11 +15,17 @@
 // 128 keys, and the halves alone overlapping, a tile took 4580 clocks at D =
 // 128, of which the tensor pipe worked 45%.)
 //
-// One persistent block per SM. Warps 0-3 and 4-7 compute the halves' softmax,
-// warp 8 fetches keys and values through a ring of tiles, warps 9 and 10 issue
-// the products of one half each, warp 11 fetches the next item's queries as
-// soon as the last scores of this one are done. A warp whose row's maximum has grown rescales its rows of O_h
-// itself, after the products of the previous step (its o_done).
+// A row's 64 scores of a step belong to two threads of two warps, which exchange
+// their maxima through shared memory. (With one thread a row, eight warps, a
+// step's chain of loads, maxima, exponentials and stores took 1850 clocks: two
+// warps a scheduler do not hide their latencies.)
+//
+// One persistent block per SM. Warps 0-7 and 8-15 compute the halves' softmax,
+// warp 16 fetches keys and values through a ring of tiles, warps 17 and 18
+// issue the products of one half each, warp 19 fetches the next item's queries
+// as soon as the last scores of this one are done. A warp whose row's maximum
+// has grown rescales its rows of O_h itself, after the products of the previous
+// step (its o_done).
 #pragma once
 
 #include "attn_rows.cuh"
@@ -32,7 +37,7 @@ namespace chunk {
 constexpr int HALF = 128;              // most rows of a half item
 constexpr int BN = 128;                // keys of a tile
 constexpr int STEP = 64;               // keys of a step: the tile's two halves
-constexpr int SOFTMAX_WARPS = 8;
+constexpr int SOFTMAX_WARPS = 16;
 constexpr int THREADS = (SOFTMAX_WARPS + 4) * 32;
 constexpr int TMEM_COLS = 512;
 template <int D>
@@ -41,9 +46,16 @@ struct Cfg {
     static constexpr int Q_BYTES = HALF * D * 2;               // one half
     static constexpr int TILE_BYTES = BN * D * 2;              // keys or values of a tile
     static constexpr int STAGES = D == 128 ? 4 : 8;
-    static constexpr int OUT_BYTES = 32 * 128;                 // staged output of one warp
-    static constexpr int SMEM_BYTES =
-        1024 + 2 * Q_BYTES + STAGES * TILE_BYTES + SOFTMAX_WARPS * OUT_BYTES;
+    static constexpr int OUT_BYTES = 32 * 64;                  // staged output of one warp
+    static constexpr int MAX_BYTES = 2 * 2 * HALF * 4;         // exchanged maxima
+    static constexpr int BARRIERS = 2 * STAGES + 18;
+    // shared memory, all of it dynamic: queries, ring, staged output, maxima,
+    // barriers, TMEM address and abort flag
+    static constexpr int RING_AT = 2 * Q_BYTES;
+    static constexpr int OUT_AT = RING_AT + STAGES * TILE_BYTES;
+    static constexpr int MAX_AT = OUT_AT + SOFTMAX_WARPS * OUT_BYTES;
+    static constexpr int BAR_AT = MAX_AT + MAX_BYTES;
+    static constexpr int SMEM_BYTES = BAR_AT + BARRIERS * 8 + 16;
 };
 
 // True in one lane of the warp. A branch on it (rather than on a lane number)
@@ -121,34 +133,6 @@ __device__ __forceinline__ void loaded32(uint32_t *r)
                    "+r"(r[30]), "+r"(r[31]));
 }
 
-// Two fp32 lanes of one 64-bit register: a multiply-add or an add of both is
-// one instruction.
-__device__ __forceinline__ uint64_t pair(float lo, float hi)
-{
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-    return d;
-}
-
-__device__ __forceinline__ void unpair(uint64_t v, float &lo, float &hi)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
 // 2^x of two lanes on the multiply-add pipe, for -126 <= x < 127: x = n + f with
 // n the nearest integer (the low bits of x + 1.5 * 2^23), 2^f by the degree-4
 // polynomial of least relative error on [-1/2, 1/2] (2.7e-6, Remez exchange),
@@ -160,8 +144,8 @@ __device__ __forceinline__ void exp2_poly2(uint64_t x, float &lo, float &hi)
     unpair(x, a, b);
     x = pair(fmaxf(a, -126.0f), fmaxf(b, -126.0f));
     const uint64_t r = add2(x, pair(12582912.0f, 12582912.0f));
-    const uint64_t f = add2(x, add2(pair(12582912.0f, 12582912.0f),
-                                    r ^ 0x8000000080000000ull));
+    const uint64_t n = add2(r, pair(-12582912.0f, -12582912.0f));
+    const uint64_t f = fma2(n, pair(-1.0f, -1.0f), x);
     uint64_t q = fma2(pair(0.009570102207362652f, 0.009570102207362652f), f,
                       pair(0.05591785907745361f, 0.05591785907745361f));
     q = fma2(q, f, pair(0.240247443318367f, 0.240247443318367f));
@@ -214,19 +198,19 @@ __global__ void __launch_bounds__(THREADS, 1)
     using C = Cfg<D>;
     using Cursor = paged::Cursor<BN>;
 
-    extern __shared__ uint8_t smem_raw[];
-    __shared__ __align__(8) uint64_t bars[2 * C::STAGES + 18];
-    __shared__ uint32_t tmem_slot;
-    __shared__ int abort_word;
-
+    // The swizzled tiles start on 1024-byte boundaries: the kernel has no other
+    // shared memory, so the array begins where the block's does.
+    extern __shared__ __align__(1024) char smem[];
     const int lane = threadIdx.x & 31;
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
-    const uint32_t smem0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t smem0 = smem_u32(smem);
     const uint32_t q_smem = smem0;                             // [half][column block][row][128 B]
-    const uint32_t ring = smem0 + 2 * C::Q_BYTES;              // [stage][column block][key][128 B]
-    int64_t *sums = reinterpret_cast<int64_t *>(smem_raw + (smem0 - smem_u32(smem_raw)));
-    volatile int *abort_flag = &abort_word;
-    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    const uint32_t ring = smem0 + C::RING_AT;                  // [stage][column block][key][128 B]
+    int64_t *sums = reinterpret_cast<int64_t *>(smem);         // while the work is dealt
+    volatile uint32_t *tmem_slot =
+        reinterpret_cast<volatile uint32_t *>(smem + C::BAR_AT + C::BARRIERS * 8);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    auto bar = [&](int i) { return smem0 + C::BAR_AT + i * 8; };
     auto full = [&](int s) { return bar(s); };
     auto empty = [&](int s) { return bar(C::STAGES + s); };
     auto q_ready = [&](int h) { return bar(2 * C::STAGES + h); };
@@ -251,18 +235,18 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int b = 0; b < 2; ++b) {
                 mbar_init(o_done(h, b), 1);
                 mbar_init(s_full(h, b), 1);
-                mbar_init(p_ready(h, b), 4);
+                mbar_init(p_ready(h, b), 8);
             }
         }
         fence_barrier_init();
-        abort_word = 0;
+        *abort_flag = 0;
     }
-    if (warp == 9)
-        tmem_alloc(smem_u32(&tmem_slot), TMEM_COLS);
+    if (warp == 17)
+        tmem_alloc(smem0 + C::BAR_AT + C::BARRIERS * 8, TMEM_COLS);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem = *tmem_slot;
     pdl_wait();
     pdl_launch_dependents();
     const paged::Work &w = p.work;
@@ -298,7 +282,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 
     paged::PartHeader head[2] = {};
     int64_t left = count;
-    if (warp == 8) {
+    if (warp == 16) {
         // ================================================ keys and values
         const int page = 1 << w.seqs.page_shift;
         const int box = min(page, BN), subs = BN / box, boxes = subs * C::CH;
@@ -346,12 +330,12 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int s = 0; s < C::STAGES; ++s)
                 if ((armed >> s) & 1u)
                     drain_wait(full(s), s < st ? ph : ph ^ 1u, p.wait_limit_ns);
-    } else if (warp == 9 || warp == 10) {
+    } else if (warp == 17 || warp == 18) {
         // ============================================== products of half h
         constexpr uint32_t S_IDESC = idesc_bf16(HALF, STEP, false);
         constexpr uint32_t O_IDESC = idesc_bf16(HALF, D, true);
         constexpr uint32_t STEP_OFF = STEP * 128 / 16;         // 64 keys further, in 16 bytes
-        const int h = warp - 9;
+        const int h = warp - 17;
         const uint64_t q_desc = smem_desc_k128_sw128(q_smem + h * C::Q_BYTES);
         const uint64_t k_desc = smem_desc_k128_sw128(ring);
         const uint64_t v_desc = smem_desc_mn_sw128(ring, BN * 128);
@@ -476,11 +460,20 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
     } else if (warp < SOFTMAX_WARPS) {
         // ======================================================== softmax
-        const int h = warp >> 2;
+        const int h = warp >> 3;                               // half of the item
+        const int part = (warp >> 2) & 1;                      // 32 of the step's 64 keys
         const int in_half = (warp & 3) * 32 + lane;
         const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t s_addr = s_tmem(h, 0) + lane_off, o_addr = o_tmem(h) + lane_off;
-        const uint32_t out = ring + C::STAGES * C::TILE_BYTES + warp * C::OUT_BYTES;
+        const uint32_t s_addr = s_tmem(h, 0) + lane_off + part * 32;
+        const uint32_t p_addr = s_tmem(h, 0) + lane_off + part * 16;
+        const uint32_t o_addr = o_tmem(h) + lane_off + part * (D / 2);
+        char *out = smem + C::OUT_AT + warp * C::OUT_BYTES;
+        const int pair_bar = 1 + h * 4 + (warp & 3);           // the two warps of 32 rows
+        // the two threads' maxima of a row, [step parity][half][row][part] in bf16
+        uint16_t *const my_max =
+            reinterpret_cast<uint16_t *>(smem + C::MAX_AT) + (h * HALF + in_half) * 2 + part;
+        const uint32_t *const both_max =
+            reinterpret_cast<const uint32_t *>(smem + C::MAX_AT) + h * HALF + in_half;
         uint32_t ph = 0;                                       // parity of the tile's barriers
         bool ok = true;
         while (ok && left > 0) {
@@ -498,48 +491,62 @@ __global__ void __launch_bounds__(THREADS, 1)
             const int end = min(rows, (h + 1) * half_rows);
             const int rr = cur.m * w.item_rows + r;
             const int tok = w.by_group(rr);
+            // a warp without a row leaves its lanes of P as they are: they only
+            // reach rows of O that nobody reads
+            const bool idle = r - lane >= end;
             float m = -INFINITY, l = 0.0f;
             if (active) {
                 const int seen_hi = cur.v.kv - cur.v.qlen + tok;     // last key the row sees
-                // keys that every row of this warp sees: tiles inside need no mask
+                // keys that every row of this warp sees: steps inside need no mask
                 const int all_hi = __shfl_sync(0xffffffffu, seen_hi, 0);
                 const int all_lo =
                     w.window > 0 ? __shfl_sync(0xffffffffu, seen_hi, 31) - w.window + 1 : 0;
                 for (int j = 0; j < 2 * nt; ++j) {
                     const int b = j & 1;
-                    if (!wait(s_full(h, b), ph)) {
-                        ok = false;
-                        break;
+                    ok = ok && wait(s_full(h, b), ph);
+                    if (idle) {                                // no row to compute
+                        if (!ok)
+                            break;
+                        ph ^= static_cast<uint32_t>(b);
+                        if (lane == 0)
+                            mbar_arrive(p_ready(h, b));
+                        continue;
                     }
                     tc_fence_after_sync();
-                    uint32_t s[STEP];
-#pragma unroll
-                    for (int c = 0; c < STEP / 32; ++c)
-                        tmem_ld_32x32b_x32(s_addr + b * STEP + c * 32,
-                                           *reinterpret_cast<uint32_t(*)[32]>(s + c * 32));
+                    uint32_t s[32];
+                    tmem_ld_32x32b_x32(s_addr + b * STEP, s);
                     tmem_ld_wait();
-#pragma unroll
-                    for (int c = 0; c < STEP / 32; ++c)
-                        loaded32(s + c * 32);
+                    loaded32(s);
                     const int key0 = cur.tile * BN + j * STEP;
                     const bool masked = key0 + STEP - 1 > all_hi || key0 < all_lo;
                     if (masked) {
-                        const int hi = seen_hi - key0;
+                        const int hi = seen_hi - key0 - part * 32;
                         const int lo = w.window > 0 ? hi - w.window : -1;
 #pragma unroll
-                        for (int i = 0; i < STEP; ++i)
+                        for (int i = 0; i < 32; ++i)
                             if (i > hi || i <= lo)
                                 s[i] = 0xff800000u;
                     }
                     float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < STEP; i += 8)
+                    for (int i = 0; i < 32; i += 8)
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             t4[k] = max3(__uint_as_float(s[i + 2 * k]),
                                          __uint_as_float(s[i + 2 * k + 1]), t4[k]);
-                    const float top =
-                        fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * p.scale_log2;
+                    // The row's maximum from both its threads, rounded to bf16 (m
+                    // need not be the maximum itself, only the same in both and
+                    // near it). The barrier also takes the two warps' verdict on
+                    // their waits, so that neither is left alone at the next one.
+                    my_max[b * 4 * HALF] = __bfloat16_as_ushort(
+                        __float2bfloat16_rn(fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]))));
+                    ok = named_bar_and(pair_bar, 64, ok);
+                    if (!ok)
+                        break;
+                    const uint32_t mx = both_max[b * 2 * HALF];
+                    const float top = fmaxf(__uint_as_float(mx << 16),
+                                            __uint_as_float(mx & 0xffff0000u)) *
+                                      p.scale_log2;
                     const bool raise = top > m + RESCALE_AT;           // also from -inf
                     if (__any_sync(0xffffffffu, raise)) {
                         const float f = raise ? exp2_approx(m - top) : 1.0f;
@@ -548,14 +555,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                         l *= f;
                         if (j > 0) {
                             // O_h rests after the last step's products (those of
-                            // the step before went ahead of this step's scores)
-                            if (!wait(o_done(h, b ^ 1), b == 1 ? ph : ph ^ 1u)) {
-                                ok = false;
-                                break;
-                            }
+                            // the step before went ahead of this step's scores);
+                            // each of the two warps rescales half its channels
+                            ok = wait(o_done(h, b ^ 1), b == 1 ? ph : ph ^ 1u);
                             tc_fence_after_sync();
 #pragma unroll 1
-                            for (int c = 0; c < D / 16; ++c) {
+                            for (int c = 0; ok && c < D / 32; ++c) {
                                 uint32_t o[16];
                                 tmem_ld_x16(o_addr + c * 16, o);
 #pragma unroll
@@ -569,30 +574,26 @@ __global__ void __launch_bounds__(THREADS, 1)
                     const float sub = m == -INFINITY ? 0.0f : m;
                     const uint64_t scale2 = pair(p.scale_log2, p.scale_log2);
                     const uint64_t sub2 = pair(-sub, -sub);
-                    uint64_t sum[4] = {0, 0, 0, 0};
+                    uint64_t sum[2] = {0, 0};
                     auto weights = [&](auto exact) {
+                        uint32_t e[16];
 #pragma unroll
-                        for (int c = 0; c < STEP / 32; ++c) {
-                            uint32_t e[16];
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const uint64_t x =
-                                    fma2(pair(__uint_as_float(s[c * 32 + 2 * i]),
-                                              __uint_as_float(s[c * 32 + 2 * i + 1])),
-                                         scale2, sub2);
-                                float a, b;
-                                if (!decltype(exact)::value && i % 4 == 3) {
-                                    exp2_poly2(x, a, b);
-                                } else {
-                                    unpair(x, a, b);
-                                    a = exp2_approx(a);
-                                    b = exp2_approx(b);
-                                }
-                                sum[i & 3] = add2(sum[i & 3], pair(a, b));
-                                e[i] = pack_bf16(a, b);
+                        for (int i = 0; i < 16; ++i) {
+                            const uint64_t x = fma2(
+                                pair(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])),
+                                scale2, sub2);
+                            float a, b;
+                            if (!decltype(exact)::value && i % 4 == 3) {
+                                exp2_poly2(x, a, b);
+                            } else {
+                                unpair(x, a, b);
+                                a = exp2_approx(a);
+                                b = exp2_approx(b);
                             }
-                            tmem_st_x16(s_addr + b * STEP + c * 16, e);
+                            sum[i & 1] = add2(sum[i & 1], pair(a, b));
+                            e[i] = pack_bf16(a, b);
                         }
+                        tmem_st_x16(p_addr + b * STEP, e);
                     };
                     // a masked score is -inf and must weigh exactly nothing
                     if (masked)
@@ -605,73 +606,77 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (lane == 0)
                         mbar_arrive(p_ready(h, b));
                     float a, c;
-                    unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), a, c);
+                    unpair(add2(sum[0], sum[1]), a, c);
                     l += a + c;
                 }
             }
-            if (!ok)
-                break;
             if (active) {
-                if (!wait(o_done(h, 1), ph ^ 1u)) {            // the last products
-                    ok = false;
-                    break;
+                // the last products; the row's sum from both its threads
+                ok = ok && wait(o_done(h, 1), ph ^ 1u);
+                if (!idle) {
+                    reinterpret_cast<float *>(out)[lane] = l;
+                    ok = named_bar_and(pair_bar, 64, ok);
+                    const float *other = reinterpret_cast<const float *>(
+                        smem + C::OUT_AT + (warp ^ 4) * C::OUT_BYTES);
+                    l = part == 0 ? l + other[lane] : other[lane] + l;
+                    ok = named_bar_and(pair_bar, 64, ok);      // both sums are read
                 }
+                if (!ok)
+                    break;
                 tc_fence_after_sync();
+            }
+            if (active && !idle) {
                 const float f = whole ? inv_sum(l) : 1.0f;
                 const int64_t slot_row = static_cast<int64_t>(slot) * p.parts.row_cap;
-                char *dst[8];                                  // of the rows that this lane writes
+                // This warp's half of the channels, 64 bytes of each row at a
+                // time through its staging rows, from where four lanes write a
+                // row's 64 bytes.
+                char *dst[4];                                  // of the rows that this lane writes
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int at = r - lane + i * 4 + (lane >> 3);
-                    dst[i] = whole ? reinterpret_cast<char *>(p.y + row_of(cur, at, p.y_stride))
-                                   : reinterpret_cast<char *>(p.parts.o + (slot_row + at) * D);
-                    dst[i] = at < end ? dst[i] + (lane & 7) * 16 : nullptr;
+                for (int i = 0; i < 4; ++i) {
+                    const int at = r - lane + i * 8 + (lane >> 2);
+                    dst[i] = whole ? reinterpret_cast<char *>(p.y + row_of(cur, at, p.y_stride) +
+                                                              part * (D / 2))
+                                   : reinterpret_cast<char *>(p.parts.o + (slot_row + at) * D +
+                                                              part * (D / 2));
+                    dst[i] = at < end ? dst[i] + (lane & 3) * 16 : nullptr;
                 }
-                // 128 bytes of each row at a time through the warp's staging
-                // rows, from where eight lanes write a row's 128 bytes
+                uint4 *const mine = reinterpret_cast<uint4 *>(out + lane * 64);
                 const int chunks = whole ? D / 64 : D / 32;
 #pragma unroll 1
                 for (int c = 0; c < chunks; ++c) {
-                    uint32_t x[32];
+                    uint32_t x[16];
                     if (whole) {
                         uint32_t o[32];
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            tmem_ld_32x32b_x32(o_addr + c * 64 + k * 32, o);
-                            tmem_ld_wait();
-                            loaded32(o);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                x[k * 16 + i] = pack_bf16(__uint_as_float(o[2 * i]) * f,
-                                                          __uint_as_float(o[2 * i + 1]) * f);
-                        }
-                    } else {
-                        tmem_ld_32x32b_x32(o_addr + c * 32, x);
+                        tmem_ld_32x32b_x32(o_addr + c * 32, o);
                         tmem_ld_wait();
-                        loaded32(x);
+                        loaded32(o);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            x[i] = pack_bf16(__uint_as_float(o[2 * i]) * f,
+                                             __uint_as_float(o[2 * i + 1]) * f);
+                    } else {
+                        tmem_ld_x16(o_addr + c * 16, x);
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                         out + lane * 128 + ((i ^ (lane & 7)) << 4)),
-                                     "r"(x[4 * i]), "r"(x[4 * i + 1]), "r"(x[4 * i + 2]),
-                                     "r"(x[4 * i + 3])
-                                     : "memory");
+                    for (int i = 0; i < 4; ++i)
+                        mine[i ^ ((lane >> 1) & 3)] =
+                            make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
                     __syncwarp();
+                    uint4 v[4];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int at = i * 4 + (lane >> 3);            // row of the warp
-                        uint4 v;
-                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                                     : "r"(out + at * 128 + (((lane & 7) ^ (at & 7)) << 4))
-                                     : "memory");
-                        if (dst[i] != nullptr)
-                            *reinterpret_cast<uint4 *>(dst[i] + c * 128) = v;
+                    for (int i = 0; i < 4; ++i) {
+                        const int at = i * 8 + (lane >> 2);            // row of the warp
+                        v[i] = reinterpret_cast<const uint4 *>(
+                            out + at * 64)[(lane & 3) ^ ((at >> 1) & 3)];
                     }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (dst[i] != nullptr)
+                            *reinterpret_cast<uint4 *>(dst[i] + c * 64) = v[i];
                     __syncwarp();
                 }
-                if (r < end) {
+                if (r < end && part == 0) {
                     if (!whole)
                         p.parts.ml[slot_row + r] = make_float2(m, l);
                     else if (p.lse != nullptr)
@@ -725,12 +730,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
-    if (warp == 9) {
+    if (warp == 17) {
         tmem_relinquish();
         tmem_dealloc(tmem, TMEM_COLS);
     }
     if (threadIdx.x == 0) {
-        if (abort_word)
+        if (*abort_flag)
             head[0].rows = head[1].rows = 0;
         p.parts.headers[2 * worker] = head[0];
         p.parts.headers[2 * worker + 1] = head[1];

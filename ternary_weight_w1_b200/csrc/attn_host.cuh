@@ -332,7 +332,7 @@ extern "C" int bitlinear_rope_append(const void *q_dev, int64_t q_stride, const 
     p.kv_heads = static_cast<int>(cache->kv_heads);
     // a row per block until every SM has a few, then several
     p.per_block = static_cast<int>(
-        std::min<int64_t>(4, std::max<int64_t>(1, tokens / (8 * dev->sms))));
+        std::min<int64_t>(rope::MAX_ROWS, std::max<int64_t>(1, tokens / (4 * dev->sms))));
     const int grid = static_cast<int>((tokens + p.per_block - 1) / p.per_block);
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     return launch_status(D == 64 ? launch_rope<64>(p, interleaved != 0, grid, st)

@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr int NT = D / 8;              // 8-channel tiles of the output
     using Cursor = paged::Cursor<BN>;
 
-    extern __shared__ uint8_t smem_raw[];
+    extern __shared__ char smem_raw[];
     __shared__ int64_t sums[paged::MAX_GROUPS];
     __shared__ __align__(8) uint64_t bars[WARPS][C::STAGES];
     __shared__ int abort_word;

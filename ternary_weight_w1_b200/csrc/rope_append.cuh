@@ -9,12 +9,15 @@
 // The kernel reads and writes every element once and is bound by memory for
 // prompts and by its launch for a few tokens. A block takes `per_block` rows:
 // its warps find the rows' sequences and compute the rows' cosines and sines
-// once into shared memory (the head count is what shares them), then every
-// thread takes 16 channels of one head, eight pairs, as two 16-byte loads, so
-// a pair never leaves a thread and a head's sum of squares is a shuffle over
-// D / 16 threads. The angle p f is taken in double and reduced by whole turns
-// there: at position 10^5 an fp32 product would already be off by several
-// thousandths of a turn. sinf and cosf then see |angle| <= pi.
+// once into shared memory (the head count is what shares them). A thread keeps
+// 16 channels, 8 c .. and D / 2 + 8 c .., which are eight whole pairs in either
+// order, and takes them of every head of its share, so a row's cosines and sines are read from shared memory once
+// per thread, a pair never leaves a thread, and a head's sum of squares is a
+// shuffle over D / 16 threads. Its next heads are on their way to shared memory
+// meanwhile, each thread's to its own place, so no barrier is needed. The angle p f is taken
+// in double and reduced by whole turns there: at position 10^5 an fp32 product
+// would already be off by several thousandths of a turn. sinf and cosf then see
+// |angle| <= pi.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -25,8 +28,9 @@
 namespace bitlinear {
 namespace rope {
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 128;
 constexpr int MAX_ROWS = 8;            // rows of a block
+constexpr int STAGES = 6;              // units that a thread has in flight, and one
 
 struct Params {
     const uint16_t *q, *k, *v;
@@ -63,26 +67,44 @@ __device__ __forceinline__ int find_seq(const paged::Seqs &q, int t)
     return __ldg(q.q_start + lo) <= t ? lo : -1;
 }
 
-// eight bf16 at p as fp32
-__device__ __forceinline__ void unpack8(const uint4 &raw, float *v)
+// eight bf16 as four pairs of fp32
+__device__ __forceinline__ void unpack8(const uint4 &raw, uint64_t *v)
 {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(w[i] << 16);
-        v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
+    for (int i = 0; i < 4; ++i)
+        v[i] = pair(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
 
-__device__ __forceinline__ uint4 pack8(const float *v)
+__device__ __forceinline__ uint4 pack8(const uint64_t *v)
 {
     uint32_t w[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&b);
+        float a, b;
+        unpair(v[i], a, b);
+        const __nv_bfloat162 x = __floats2bfloat162_rn(a, b);
+        w[i] = *reinterpret_cast<const uint32_t *>(&x);
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Shared arrays of eight pairs for each of T threads are kept in 16-byte pieces,
+// piece q of thread c at (q * T + c) * 16, so that neighbours read neighbouring
+// pieces. Element e of thread c:
+template <int T>
+__device__ __forceinline__ int piece_at(int c, int e)
+{
+    return ((e >> 2) * T + c) * 4 + (e & 3);
+}
+
+// pairs 2 q, 2 q + 1 of thread c
+template <int T>
+__device__ __forceinline__ void load_pairs(const float *p, int c, int q, uint64_t *v)
+{
+    const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(p + (q * T + c) * 4);
+    v[0] = x.x;
+    v[1] = x.y;
 }
 
 template <int D, bool INTERLEAVED>
@@ -90,7 +112,14 @@ __global__ void __launch_bounds__(THREADS) rope_append_kernel(const Params p)
 {
     constexpr int TPH = D / 16;             // threads per head
     constexpr int HALF = D / 2;
-    __shared__ float cs[MAX_ROWS][2][HALF];
+    constexpr int HPB = THREADS / TPH;      // heads a pass of the block
+    // A row's factors as the products below take them, in pieces (piece_at):
+    // cosines and sines of the thread's eight pairs, or for interleaved pairs
+    // each cosine twice and each sine as (-sin, sin).
+    __shared__ __align__(16) float cosines[MAX_ROWS][INTERLEAVED ? D : HALF];
+    __shared__ __align__(16) float sines[MAX_ROWS][INTERLEAVED ? D : HALF];
+    __shared__ __align__(16) float gains[2][D];         // of the queries, of the keys
+    __shared__ uint4 staged[STAGES][2][THREADS];        // a thread's own next units
     __shared__ int64_t slot[MAX_ROWS];      // the row's element offset in the caches (head 0), -1: none
     __shared__ int posn[MAX_ROWS];          // the row's position, -1: no row of a sequence
 
@@ -98,27 +127,34 @@ __global__ void __launch_bounds__(THREADS) rope_append_kernel(const Params p)
     pdl_launch_dependents();
     const int t0 = blockIdx.x * p.per_block;
     const int rows = min(p.per_block, p.seqs.tokens - t0);
-    const int warp = threadIdx.x >> 5;
-    if (warp < rows) {
-        const int t = t0 + warp;
+    for (int i = threadIdx.x; i < 2 * D; i += THREADS) {
+        const float *gain = i < D ? p.q_gain : p.k_gain;
+        if (gain != nullptr) {
+            // channel e of a head belongs to thread c as its element j
+            const int e = i % D;
+            const int c = e % HALF / 8, j = e % 8 + e / HALF * 8;
+            gains[i / D][piece_at<TPH>(c, j)] = __ldg(gain + e);
+        }
+    }
+    for (int r = threadIdx.x >> 5; r < rows; r += THREADS / 32) {
+        const int t = t0 + r;
         const int s = find_seq(p.seqs, t);
-        int pos = -1;
-        int64_t at = -1;
-        if (s >= 0 && (threadIdx.x & 31) == 0) {
-            const paged::View v = paged::view(p.seqs, s);
-            pos = v.kv - (v.q0 + v.qlen - t);
+        if ((threadIdx.x & 31) == 0) {
+            int pos = -1;
+            int64_t at = -1;
+            if (s >= 0) {
+                const paged::View v = paged::view(p.seqs, s);
+                // a row before position 0 has no place
+                pos = max(v.kv - (v.q0 + v.qlen - t), -1);
+            }
             if (pos >= 0) {
                 const int page = paged::page_of(p.seqs, s, pos >> p.seqs.page_shift);
                 const int size = 1 << p.seqs.page_shift;
                 if (page >= 0)
                     at = (static_cast<int64_t>(page) * p.kv_heads * size + (pos & (size - 1))) * D;
-            } else {
-                pos = -1;                   // a row before position 0 has no place
             }
-        }
-        if ((threadIdx.x & 31) == 0) {
-            posn[warp] = pos;
-            slot[warp] = at;
+            posn[r] = pos;
+            slot[r] = at;
         }
     }
     __syncthreads();
@@ -128,76 +164,132 @@ __global__ void __launch_bounds__(THREADS) rope_append_kernel(const Params p)
             continue;
         constexpr double TURN = 6.283185307179586476925;
         const double angle = static_cast<double>(posn[r]) * static_cast<double>(__ldg(p.inv_freq + f));
-        const float a = static_cast<float>(angle - rint(angle / TURN) * TURN);
-        cs[r][0][f] = cosf(a);
-        cs[r][1][f] = sinf(a);
+        const float a = static_cast<float>(angle - rint(angle * (1.0 / TURN)) * TURN);
+        const float co = cosf(a), si = sinf(a);
+        if (INTERLEAVED) {
+            // pair f is channels 2 f and 2 f + 1 of one 16-byte chunk
+            const int c = f / 4 % TPH, j = f % 4 + f / 4 / TPH * 4;
+            cosines[r][piece_at<TPH>(c, 2 * j)] = cosines[r][piece_at<TPH>(c, 2 * j + 1)] = co;
+            sines[r][piece_at<TPH>(c, 2 * j)] = -si;
+            sines[r][piece_at<TPH>(c, 2 * j + 1)] = si;
+        } else {
+            const int c = f / 8, j = f % 8;
+            cosines[r][piece_at<TPH>(c, j)] = co;
+            sines[r][piece_at<TPH>(c, j)] = si;
+        }
     }
     __syncthreads();
 
     const int heads = p.q_heads + 2 * p.kv_heads;
     const int64_t head_step = static_cast<int64_t>(D) << p.seqs.page_shift;
-    for (int i = threadIdx.x; i < rows * heads * TPH; i += THREADS) {
-        const int c = i % TPH;
-        const int rh = i / TPH;
-        const int r = rh / heads;
-        const int h = rh - r * heads;
-        // a head's threads share r and h, so they skip it together
-        if (posn[r] < 0)
-            continue;
+    const int c = threadIdx.x % TPH;
+    const int passes = (heads + HPB - 1) / HPB;
+    const int units = rows * passes;        // head h0 + pass * HPB of a row, row after row
+    const int h0 = threadIdx.x / TPH;
+    // where unit (r, h) of this thread is read; null when there is none
+    auto source = [&](int r, int h) -> const uint16_t * {
+        if (h >= heads || posn[r] < 0)
+            return nullptr;
         const int64_t t = t0 + r;
-        const bool is_q = h < p.q_heads;
-        const int hk = is_q ? 0 : (h - p.q_heads) % p.kv_heads;
-        const bool is_v = h >= p.q_heads + p.kv_heads;
-        const uint16_t *src = is_q ? p.q + t * p.q_stride + h * D
-                                   : is_v ? p.v + t * p.v_stride + hk * D
-                                          : p.k + t * p.k_stride + hk * D;
-        uint16_t *dst;
-        if (is_q)
-            dst = p.q_out + t * p.q_out_stride + h * D;
-        else
-            dst = slot[r] < 0 ? nullptr : (is_v ? p.v_cache : p.k_cache) + slot[r] + hk * head_step;
-        const int e0 = INTERLEAVED || is_v ? 16 * c : 8 * c;
-        const int e1 = INTERLEAVED || is_v ? 16 * c + 8 : HALF + 8 * c;
-        uint4 lo = *reinterpret_cast<const uint4 *>(src + e0);
-        uint4 hi = *reinterpret_cast<const uint4 *>(src + e1);
-        if (!is_v) {
-            float x[16];
-            unpack8(lo, x);
-            unpack8(hi, x + 8);
-            const float *gain = is_q ? p.q_gain : p.k_gain;
-            if (gain != nullptr) {
-                float ss = 0.0f;
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    ss = fmaf(x[j], x[j], ss);
-                const unsigned mask = (TPH == 8 ? 0xffu : 0xfu)
-                                      << ((threadIdx.x & 31) & ~(TPH - 1));
-#pragma unroll
-                for (int o = TPH / 2; o > 0; o >>= 1)
-                    ss += __shfl_xor_sync(mask, ss, o);
-                const float rs = __fdiv_rn(
-                    1.0f, __fsqrt_rn(ss * (1.0f / D) + p.eps));
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    x[j] = norm1(x[j], rs, __ldg(gain + e0 + j));
-                    x[8 + j] = norm1(x[8 + j], rs, __ldg(gain + e1 + j));
-                }
+        return h < p.q_heads ? p.q + t * p.q_stride + h * D
+               : h < p.q_heads + p.kv_heads
+                   ? p.k + t * p.k_stride + (h - p.q_heads) * D
+                   : p.v + t * p.v_stride + (h - p.q_heads - p.kv_heads) * D;
+    };
+    int fr = 0, fh = h0, fn = 0;            // next unit to fetch
+    auto fetch = [&]() {
+        if (fn < units) {
+            const uint16_t *src = source(fr, fh);
+            if (src != nullptr) {
+                const uint32_t dst = smem_u32(&staged[fn % STAGES][0][threadIdx.x]);
+                cp_async16(dst, src + 8 * c);
+                cp_async16(dst + THREADS * 16, src + HALF + 8 * c);
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float &a = INTERLEAVED ? x[2 * j] : x[j];
-                float &b = INTERLEAVED ? x[2 * j + 1] : x[8 + j];
-                const float co = cs[r][0][8 * c + j], si = cs[r][1][8 * c + j];
-                const float u = a * co - b * si;
-                b = b * co + a * si;
-                a = u;
+            ++fn;
+            fh += HPB;
+            if (fh >= passes * HPB) {
+                fh = h0;
+                ++fr;
             }
-            lo = pack8(x);
-            hi = pack8(x + 8);
         }
-        if (dst != nullptr) {
-            *reinterpret_cast<uint4 *>(dst + e0) = lo;
-            *reinterpret_cast<uint4 *>(dst + e1) = hi;
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+#pragma unroll
+    for (int i = 0; i < STAGES - 1; ++i)
+        fetch();
+    constexpr int FACTORS = INTERLEAVED ? 8 : 4;        // pairs of cosines (sines)
+    uint64_t co[FACTORS], si[FACTORS];
+    for (int r = 0, n = 0; r < rows; ++r) {
+        const int64_t t = t0 + r;
+        const int64_t at = slot[r];
+#pragma unroll
+        for (int q = 0; q < FACTORS / 2; ++q) {
+            load_pairs<TPH>(cosines[r], c, q, co + 2 * q);
+            load_pairs<TPH>(sines[r], c, q, si + 2 * q);
+        }
+        for (int h = h0; h < passes * HPB; h += HPB, ++n) {
+            fetch();
+            asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
+            // a head's threads share r and h, so they skip it together
+            if (h >= heads || posn[r] < 0)
+                continue;
+            uint4 lo = staged[n % STAGES][0][threadIdx.x];
+            uint4 hi = staged[n % STAGES][1][threadIdx.x];
+            const bool is_q = h < p.q_heads, is_v = h >= p.q_heads + p.kv_heads;
+            if (!is_v) {
+                uint64_t x[8];
+                unpack8(lo, x);
+                unpack8(hi, x + 4);
+                if ((is_q ? p.q_gain : p.k_gain) != nullptr) {
+                    uint64_t ss2 = mul2(x[0], x[0]);
+#pragma unroll
+                    for (int j = 1; j < 8; ++j)
+                        ss2 = fma2(x[j], x[j], ss2);
+                    float ss, other;
+                    unpair(ss2, ss, other);
+                    ss += other;
+                    const unsigned mask = (TPH == 8 ? 0xffu : 0xfu)
+                                          << ((threadIdx.x & 31) & ~(TPH - 1));
+#pragma unroll
+                    for (int o = TPH / 2; o > 0; o >>= 1)
+                        ss += __shfl_xor_sync(mask, ss, o);
+                    const float rs = __fdiv_rn(1.0f, __fsqrt_rn(ss * (1.0f / D) + p.eps));
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint64_t g[2];
+                        load_pairs<TPH>(gains[is_q ? 0 : 1], c, q, g);
+                        x[2 * q] = mul2(mul2(x[2 * q], pair(rs, rs)), g[0]);
+                        x[2 * q + 1] = mul2(mul2(x[2 * q + 1], pair(rs, rs)), g[1]);
+                    }
+                }
+                if constexpr (INTERLEAVED) {
+                    // (a, b) (cos, cos) + (b, a) (-sin, sin)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float a, b;
+                        unpair(x[j], a, b);
+                        x[j] = fma2(pair(b, a), si[j], mul2(x[j], co[j]));
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint64_t minus = si[j] ^ 0x8000000080000000ull;
+                        const uint64_t u = fma2(x[4 + j], minus, mul2(x[j], co[j]));
+                        x[4 + j] = fma2(x[j], si[j], mul2(x[4 + j], co[j]));
+                        x[j] = u;
+                    }
+                }
+                lo = pack8(x);
+                hi = pack8(x + 4);
+            }
+            if (is_q || at >= 0) {
+                uint16_t *dst =
+                    is_q ? p.q_out + t * p.q_out_stride + h * D
+                         : is_v ? p.v_cache + at + (h - p.q_heads - p.kv_heads) * head_step
+                                : p.k_cache + at + (h - p.q_heads) * head_step;
+                *reinterpret_cast<uint4 *>(dst + 8 * c) = lo;
+                *reinterpret_cast<uint4 *>(dst + HALF + 8 * c) = hi;
+            }
         }
     }
 }
