@@ -551,66 +551,55 @@ def _ffn_width(packed, K: int) -> int:
 # ------------------------------------------------- attention on a paged cache
 #
 # A decode step makes these calls once per layer around kernels of a few
-# microseconds, so their argument checks are written for speed: the common
-# case is decided by a few attribute reads per tensor, and only a tensor that
-# fails them goes through _Args, which finds the error or accepts it.
+# microseconds. Their common case is marshalled in C++ (csrc/fastcall.cpp); a
+# call that it does not take as plainly right goes through the checks below,
+# which find the error or make the call.
+
+_fast_calls = None
+
+
+def _fast():
+    global _fast_calls
+    if _fast_calls is None:
+        L = lib()
+        from . import _fastcall
+        address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
+        _fastcall.bind(address(L.bitlinear_rope_append), address(L.bitlinear_paged_attention))
+        _fast_calls = _fastcall
+    return _fast_calls
+
 
 _CACHE = struct.Struct("=2Q4q")        # bitlinear_kv_cache
 _SEQS = struct.Struct("=3Q2q")         # bitlinear_seqs
 
 
-def _dev(t, name: str, dtype, cur: int) -> int:
-    """Address of a contiguous tensor on the current device ``cur``."""
-    if t.get_device() == cur and t.dtype is dtype and t.is_contiguous():
-        return t.data_ptr()
-    return _Args().ptr(t, name, dtype)
-
-
-def _head_rows(t, name: str, T, heads, D: int, cur: int, dtype):
-    """(address, row stride, heads) of a bf16 tensor of T rows of whole heads,
-    [T][heads * D] or [T][heads][D] (T or heads None: any)."""
-    shape = t.shape
-    n = len(shape)
-    got = shape[1] if n == 3 and shape[2] == D else shape[1] // D if n == 2 else 0
-    if (got == heads or heads is None and got > 0) and (T is None or shape[0] == T) and (
-            t.get_device() == cur and t.dtype is dtype and t.is_contiguous()
-            and (n == 3 or got * D == shape[1])):
-        return t.data_ptr(), got * D, got
-    if T is not None and n > 0 and shape[0] != T:
-        raise ValueError(f"{name} must have {T} rows, got {shape[0]}")
-    return _Args().rows(t, name, heads, D)
-
-
-def _paged(k_cache, v_cache, q_start, kv_len, page_table, cur: int, torch):
+def _paged(a: _Args, k_cache, v_cache, q_start, kv_len, page_table):
     """(kv_heads, head_dim, sequences, the packed bitlinear_kv_cache and
     bitlinear_seqs) of one call: k_cache and v_cache [pages][kv_heads][page]
     [head_dim] bf16, q_start [S + 1], kv_len [S] and page_table [S][columns]
     int32."""
-    shape = k_cache.shape
-    if len(shape) != 4:
+    import torch
+    if k_cache.dim() != 4:
         raise ValueError("k_cache must be [pages][kv_heads][page][head_dim], got "
-                         f"{tuple(shape)}")
-    pages, kv_heads, page, D = shape
-    if D != 64 and D != 128:
+                         f"{tuple(k_cache.shape)}")
+    pages, kv_heads, page, D = k_cache.shape
+    if D not in (64, 128):
         raise BitLinearError(BITLINEAR_ERR_SHAPE, f"k_cache with head_dim {D}")
-    if v_cache.shape != shape:
-        raise ValueError(f"v_cache must have shape {tuple(shape)}, got {tuple(v_cache.shape)}")
     if page_table.dim() != 2:
         raise ValueError(f"page_table must be [S][columns], got {tuple(page_table.shape)}")
     S, cols = page_table.shape
-    if q_start.shape != (S + 1,) or kv_len.shape != (S,):
-        raise ValueError(f"q_start and kv_len must have shapes ({S + 1},) and ({S},), got "
-                         f"{tuple(q_start.shape)} and {tuple(kv_len.shape)}")
     bf16, i32 = torch.bfloat16, torch.int32
     return (kv_heads, D, S,
-            _CACHE.pack(_dev(k_cache, "k_cache", bf16, cur), _dev(v_cache, "v_cache", bf16, cur),
-                        pages, kv_heads, page, D),
-            _SEQS.pack(_dev(q_start, "q_start", i32, cur), _dev(kv_len, "kv_len", i32, cur),
-                       _dev(page_table, "page_table", i32, cur), S, cols))
+            _CACHE.pack(a.ptr(k_cache, "k_cache", bf16),
+                        a.ptr(v_cache, "v_cache", bf16, k_cache.shape), pages, kv_heads, page, D),
+            _SEQS.pack(a.ptr(q_start, "q_start", i32, (S + 1,)),
+                       a.ptr(kv_len, "kv_len", i32, (S,)), a.ptr(page_table, "page_table", i32),
+                       S, cols))
 
 
-def _raw_stream(stream, cur: int, torch) -> int:
-    return torch._C._cuda_getCurrentRawStream(cur) if stream is None else stream.cuda_stream
+def _same_rows(t, name: str, T: int):
+    if t.dim() < 1 or t.shape[0] != T:
+        raise ValueError(f"{name} must have {T} rows, got {tuple(t.shape)}")
 
 
 def _new(t, stream, shape=None, dtype=None):
@@ -637,26 +626,28 @@ def bitlinear_rope_append(q, k, v, k_cache, v_cache, q_start, kv_len, page_table
     fp32. Row i of sequence s (rows q_start[s] .. q_start[s + 1]) stands at
     position kv_len[s] - its rows + i. Returns the rotated queries (``q_out``,
     which may be ``q``; rows of no sequence are not written)."""
-    import torch
-    cur = torch._C._cuda_getDevice() if k_cache.is_cuda else -2
-    bf16, f32 = torch.bfloat16, torch.float32
-    kv_heads, D, _, cache, seqs = _paged(k_cache, v_cache, q_start, kv_len, page_table, cur, torch)
-    qp, qs, heads = _head_rows(q, "q", None, None, D, cur, bf16)
-    T = q.shape[0]
-    kp, ks, _ = _head_rows(k, "k", T, kv_heads, D, cur, bf16)
-    vp, vs, _ = _head_rows(v, "v", T, kv_heads, D, cur, bf16)
     if q_out is None:
         q_out = _new(q, stream)
-    op, os_, _ = _head_rows(q_out, "q_out", T, heads, D, cur, bf16)
-    for t, name, n in ((inv_freq, "inv_freq", D // 2), (q_gain, "q_gain", D),
-                       (k_gain, "k_gain", D)):
-        if t is not None and t.shape != (n,):
-            raise ValueError(f"{name} must have shape ({n},), got {tuple(t.shape)}")
-    rc = lib().bitlinear_rope_append(
-        qp, qs, kp, ks, vp, vs, T, heads, cache, seqs, _dev(inv_freq, "inv_freq", f32, cur),
-        1 if interleaved else 0, None if q_gain is None else _dev(q_gain, "q_gain", f32, cur),
-        None if k_gain is None else _dev(k_gain, "k_gain", f32, cur), eps, op, os_,
-        _raw_stream(stream, cur, torch))
+    rc = _fast().rope_append(q, k, v, k_cache, v_cache, q_start, kv_len, page_table, inv_freq,
+                             q_out, q_gain, k_gain, eps, interleaved,
+                             None if stream is None else stream.cuda_stream)
+    if rc is None:
+        import torch
+        a = _Args()
+        kv_heads, D, _, cache, seqs = _paged(a, k_cache, v_cache, q_start, kv_len, page_table)
+        qp, qs, heads = a.rows(q, "q", None, D)
+        T = q.shape[0]
+        for t, name in ((k, "k"), (v, "v"), (q_out, "q_out")):
+            _same_rows(t, name, T)
+        kp, ks, _ = a.rows(k, "k", kv_heads, D)
+        vp, vs, _ = a.rows(v, "v", kv_heads, D)
+        op, os_, _ = a.rows(q_out, "q_out", heads, D)
+        f32 = torch.float32
+        rc = lib().bitlinear_rope_append(
+            qp, qs, kp, ks, vp, vs, T, heads, cache, seqs,
+            a.ptr(inv_freq, "inv_freq", f32, (D // 2,)), 1 if interleaved else 0,
+            a.ptr(q_gain, "q_gain", f32, (D,)), a.ptr(k_gain, "k_gain", f32, (D,)), float(eps),
+            op, os_, _stream(stream))
     if rc:
         _check(rc, "bitlinear_rope_append")
     return q_out
@@ -682,30 +673,41 @@ def bitlinear_paged_attention(q, k_cache, v_cache, q_start, kv_len, page_table, 
     ``bitlinear_workspace_bytes_attention`` bytes (allocated here when
     omitted). Returns ``y`` (bf16, shaped like ``q``; rows that see no key are
     zero, rows of no sequence are not written)."""
-    import torch
-    cur = torch._C._cuda_getDevice() if k_cache.is_cuda else -2
-    bf16 = torch.bfloat16
-    kv_heads, D, S, cache, seqs = _paged(k_cache, v_cache, q_start, kv_len, page_table, cur, torch)
-    qp, qs, heads = _head_rows(q, "q", None, None, D, cur, bf16)
-    T = q.shape[0]
     if y is None:
         y = _new(q, stream)
-    yp, ys, _ = _head_rows(y, "y", T, heads, D, cur, bf16)
-    if lse is not None and lse.shape != (T, heads):
-        raise ValueError(f"lse must have shape ({T}, {heads}), got {tuple(lse.shape)}")
     if workspace is None:
-        need = bitlinear_workspace_bytes_attention(T, S, heads, kv_heads, D)
-        if need == ctypes.c_size_t(-1).value:
-            raise BitLinearError(BITLINEAR_ERR_SHAPE, "bitlinear_workspace_bytes_attention")
-        workspace = _new(q, stream, (need,), torch.uint8)
-    rc = lib().bitlinear_paged_attention(
-        qp, qs, T, heads, cache, seqs, D ** -0.5 if scale is None else scale, window,
-        max_q_len or 0, yp, ys, None if lse is None else _dev(lse, "lse", torch.float32, cur),
-        _dev(workspace, "workspace", torch.uint8, cur), workspace.numel(),
-        _raw_stream(stream, cur, torch))
+        workspace = _attention_workspace(q, k_cache, page_table, stream)
+    rc = _fast().paged_attention(q, k_cache, v_cache, q_start, kv_len, page_table, scale, window,
+                                 max_q_len, y, lse, workspace,
+                                 None if stream is None else stream.cuda_stream)
+    if rc is None:
+        import torch
+        a = _Args()
+        _, D, _, cache, seqs = _paged(a, k_cache, v_cache, q_start, kv_len, page_table)
+        qp, qs, heads = a.rows(q, "q", None, D)
+        T = q.shape[0]
+        _same_rows(y, "y", T)
+        yp, ys, _ = a.rows(y, "y", heads, D)
+        rc = lib().bitlinear_paged_attention(
+            qp, qs, T, heads, cache, seqs, float(D ** -0.5 if scale is None else scale),
+            int(window), int(max_q_len or 0), yp, ys,
+            a.ptr(lse, "lse", torch.float32, (T, heads)),
+            a.ptr(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
     if rc:
         _check(rc, "bitlinear_paged_attention")
     return y
+
+
+def _attention_workspace(q, k_cache, page_table, stream):
+    """A workspace for a call without one (shapes that the call refuses get an
+    empty one: the call names the error)."""
+    import torch
+    need = 0
+    if k_cache.dim() == 4 and page_table.dim() == 2 and q.dim() > 1 and k_cache.shape[3] > 0:
+        need = bitlinear_workspace_bytes_attention(
+            q.shape[0], page_table.shape[0], q[:1].numel() // k_cache.shape[3], k_cache.shape[1],
+            k_cache.shape[3])
+    return _new(q, stream, (0 if need == ctypes.c_size_t(-1).value else need,), torch.uint8)
 
 
 def bitlinear_get_fault(stream=None) -> tuple[int, int]:

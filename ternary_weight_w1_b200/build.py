@@ -5,7 +5,8 @@
 The library is one CUDA translation unit (the kernels and the C ABI) plus
 the host packer and the packed-weight file reader and writer. cudart is
 linked statically so the library does not depend on which CUDA runtime the
-host process loaded first.
+host process loaded first. Beside it stands _fastcall.so, a Python extension
+that marshals the paged-cache calls (csrc/fastcall.cpp, built with g++).
 """
 from __future__ import annotations
 
@@ -28,6 +29,11 @@ NVCC_FLAGS = [
     "-Xcompiler", "-fPIC", "-Xcompiler", "-O3", "-Xcompiler", "-Wall,-Wextra",
     "-shared", "-cudart", "static",
 ]
+
+
+# The C++ marshalling of the paged-cache calls, built against torch's headers.
+FAST_SOURCE = os.path.join(CSRC, "fastcall.cpp")
+FAST_LIB = os.path.join(HERE, "_fastcall.so")
 
 
 def nvcc() -> str:
@@ -57,6 +63,33 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     return LIB
 
 
+def build_fastcall(force: bool = False, verbose: bool = False) -> str:
+    deps = (FAST_SOURCE, os.path.join(HERE, "..", "include", "bitlinear.h"))
+    if not force and os.path.exists(FAST_LIB) and all(
+            os.path.getmtime(FAST_LIB) >= os.path.getmtime(d) for d in deps):
+        return FAST_LIB
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           *(f"-isystem{d}" for d in (f"{root}/include",
+                                      f"{root}/include/torch/csrc/api/include",
+                                      f"{cuda}/include", sysconfig.get_paths()["include"])),
+           FAST_SOURCE, "-o", FAST_LIB + ".tmp", f"-L{root}/lib", "-ltorch_python", "-ltorch",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + r.stdout + r.stderr)
+    os.replace(FAST_LIB + ".tmp", FAST_LIB)
+    return FAST_LIB
+
+
 if __name__ == "__main__":
     build(force="--force" in sys.argv, verbose=True,
           extra=["-Xptxas", "-v"] if "--ptxas" in sys.argv else ())
+    build_fastcall(force="--force" in sys.argv, verbose=True)
