@@ -172,8 +172,9 @@ struct AttnLayout {
 AttnLayout attn_layout(int64_t rows, int64_t head_dim, char *base)
 {
     AttnLayout l{};
-    l.bytes = parts_layout(kAttnMaxGrid * attn::rows::WARPS, std::min<int64_t>(rows, kRowsKernelMax),
-                           head_dim, base, &l.rows);
+    const int blocks = head_dim == 64 ? attn::rows::Cfg<64>::BLOCKS : attn::rows::Cfg<128>::BLOCKS;
+    l.bytes = parts_layout(kAttnMaxGrid * blocks * attn::rows::WARPS,
+                           std::min<int64_t>(rows, kRowsKernelMax), head_dim, base, &l.rows);
     if (rows > kRowsKernelMax)
         l.bytes += parts_layout(kAttnMaxGrid, std::min<int64_t>(rows, 2 * attn::chunk::HALF), head_dim,
                                 base + l.bytes, &l.chunk);
@@ -184,11 +185,10 @@ int launch_merge(const attn::Params &p, int64_t head_dim, int workers, const Dev
                  cudaStream_t st)
 {
     const attn::MergeParams m{p.parts, p.y, p.y_stride, p.lse, p.q_heads, p.work, workers};
-    static_assert(kAttnMaxGrid * attn::rows::WARPS <= attn::MERGE_MAX_WORKERS);
-    // one wave at most, and no more blocks than there are rows
-    const int64_t rows = static_cast<int64_t>(p.work.seqs.tokens) * p.q_heads;
-    const dim3 grid(static_cast<unsigned>(std::min<int64_t>(rows, dev.sms))),
-        block(attn::MERGE_THREADS);
+    // one wave of blocks, the items' rows dealt to them
+    const int x = (workers + attn::MERGE_WARPS - 1) / attn::MERGE_WARPS;
+    const int rows = std::min(p.work.item_rows, p.parts.row_cap);
+    const dim3 grid(x, std::max(1, std::min(rows, 2 * dev.sms / x))), block(attn::MERGE_THREADS);
     return launch_status(head_dim == 64 ? launch(attn::merge_kernel<64>, grid, block, 0, st, m)
                                         : launch(attn::merge_kernel<128>, grid, block, 0, st, m));
 }
@@ -204,7 +204,7 @@ int run_attn_rows(attn::Params p, const bitlinear_kv_cache &cache, const DeviceI
     if (!make_map_cache(&maps.k, cache.k_dev, cache, box) ||
         !make_map_cache(&maps.v, cache.v_dev, cache, box))
         return BITLINEAR_ERR_CUDA;
-    const int grid = std::min(dev.sms, kAttnMaxGrid);
+    const int grid = std::min(dev.sms, kAttnMaxGrid) * attn::rows::Cfg<D>::BLOCKS;
     cudaError_t e = allow_smem<attn::rows::attn_rows_kernel<D, MT>>(dev.id, smem);
     if (e == cudaSuccess)
         e = launch(attn::rows::attn_rows_kernel<D, MT>, dim3(grid), dim3(attn::rows::THREADS),

@@ -92,10 +92,13 @@ namespace rows {
 constexpr int WARPS = 4;
 constexpr int THREADS = WARPS * 32;
 constexpr int BN = 32;                 // keys of a slice
-constexpr int RING_BYTES = 48 * 1024;  // of one warp
 
+// One block an SM, or two for 64 channels: a slice then has half the bytes for
+// nearly the same latency, and eight warps keep as many bytes in flight.
 template <int D>
 struct Cfg {
+    static constexpr int BLOCKS = D == 64 ? 2 : 1;               // per SM
+    static constexpr int RING_BYTES = 48 * 1024 / BLOCKS;        // of one warp
     static constexpr int HALVES = D / 64;
     static constexpr int HALF_BYTES = BN * 128;
     static constexpr int TENSOR_BYTES = HALVES * HALF_BYTES;     // the slice's keys (or values)
@@ -132,7 +135,7 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], 
 
 // MT 16-row tiles per item.
 template <int D, int MT>
-__global__ void __launch_bounds__(THREADS, 1)
+__global__ void __launch_bounds__(THREADS, Cfg<D>::BLOCKS)
     attn_rows_kernel(const __grid_constant__ Maps maps, const Params p)
 {
     using C = Cfg<D>;
@@ -150,7 +153,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int worker = warp * gridDim.x + blockIdx.x;
     const int workers = WARPS * gridDim.x;
     volatile int *abort_flag = &abort_word;
-    const uint32_t ring = ((smem_u32(smem_raw) + 1023u) & ~1023u) + warp * RING_BYTES;
+    const uint32_t ring = ((smem_u32(smem_raw) + 1023u) & ~1023u) + warp * C::RING_BYTES;
     if (threadIdx.x == 0) {
         prefetch_tensormap(&maps.k);
         prefetch_tensormap(&maps.v);
@@ -176,13 +179,29 @@ __global__ void __launch_bounds__(THREADS, 1)
         Cursor ld = cur;
 
         // Lane i loads the slice's box i: tensor (k, v), half of the channels,
-        // part of the rows. A box without a needed key, or of a page that the
-        // table does not hold, starts behind the cache and is filled with zeros.
+        // part of the rows. A box without a needed key, or of a page that the table
+        // does not hold, starts behind the cache and is filled with zeros. The
+        // pages of 32 slices are looked up at a time, one slice's a lane.
         const int boxes = 2 * C::HALVES * subs;
         int64_t loaded = 0, done = 0;
         int ld_stage = 0, stage = 0;
         uint32_t parity = 0;
+        int first = 0, ahead = 0;                      // the slices looked up
+        int ids[2] = {-1, -1};                         // (two pages a slice when they are of 16)
         auto load = [&]() {
+            if (ld.tile - first >= ahead) {
+                first = ld.tile;
+                ahead = min(32, ld.t.end - first);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int key = (first + lane) * BN + i * box;
+                    ids[i] = -1;
+                    if (i < subs && key < ld.t.khi && key + box > ld.t.klo)
+                        ids[i] = paged::page_of(w.seqs, ld.s, key >> w.seqs.page_shift);
+                }
+            }
+            const int id0 = __shfl_sync(0xffffffffu, ids[0], ld.tile - first);
+            const int id1 = __shfl_sync(0xffffffffu, ids[1], ld.tile - first);
             const int st = ld_stage;
             ld_stage = ld_stage + 1 == C::STAGES ? 0 : ld_stage + 1;
             const uint32_t bar = smem_u32(&bars[warp][st]);
@@ -194,18 +213,19 @@ __global__ void __launch_bounds__(THREADS, 1)
                 const int half = (lane / subs) % C::HALVES;
                 const bool is_v = lane >= subs * C::HALVES;
                 const int key = ld.tile * BN + sub * box;
-                int row = p.cache_rows;
-                if (key < ld.t.khi && key + box > ld.t.klo) {
-                    const int id = paged::page_of(w.seqs, ld.s, key >> w.seqs.page_shift);
-                    if (id >= 0)
-                        row = ((id * w.kv_heads + ld.h) << w.seqs.page_shift) + (key & (page - 1));
-                }
+                const int id = sub == 0 ? id0 : id1;
+                const int row = id < 0 ? p.cache_rows
+                                       : ((id * w.kv_heads + ld.h) << w.seqs.page_shift) +
+                                             (key & (page - 1));
                 const uint32_t dst = ring + st * C::STAGE_BYTES + (is_v ? C::TENSOR_BYTES : 0) +
                                      half * C::HALF_BYTES + sub * box * 128;
                 tma_load_2d(dst, is_v ? &maps.v : &maps.k, half * 64, row, bar);
             }
-            if (++loaded < count && ++ld.tile == ld.t.end)
+            if (++loaded < count && ++ld.tile == ld.t.end) {
                 ld.next_item(w);
+                ahead = 0;
+                first = ld.tile;
+            }
         };
         for (int i = 0; i < C::STAGES && loaded < count; ++i)
             load();
@@ -461,27 +481,18 @@ __global__ void __launch_bounds__(THREADS, 1)
 // ------------------------------------------------------------------- merge
 //
 // Joins the parts of the items that were split between workers: o = sum_i
-// 2^(m_i - M) o_i and l likewise, M the largest m_i. Every block reads all
-// headers, lists the split items (each begins in some worker's second slot),
-// and takes its share of the jobs, groups of their rows: one wave of blocks
-// whatever the items are. (A block per worker and row group spent 15 us on
-// launching blocks that found nothing.) A warp's lanes take D / 32 channels
-// each of a row and have eight parts in flight: of one row, or of two or four
-// rows when the item has few parts. With many parts (a single token behind a long
-// context) the parts of a row are spread over the block's warps, which are then
-// added in a fixed order, so that repeated calls give the same bits.
+// 2^(m_i - M) o_i and l likewise, M the largest m_i. A split item begins in some
+// worker's second slot and goes on in the first slots of the workers behind it.
+// Block (x, y) lists the split items of workers 8 x .. 8 x + 7, one a warp, and
+// takes every gridDim.y-th of their row groups. A warp's lanes take D / 32
+// channels each of a row and have eight parts in flight: of one row, or of two
+// or four rows when the item has few parts. With many parts (a single token
+// behind a long context) the parts of a row are spread over the block's warps,
+// which are then added in a fixed order, so that repeated calls give the same
+// bits.
 
 constexpr int MERGE_WARPS = 8;
 constexpr int MERGE_THREADS = MERGE_WARPS * 32;
-constexpr int MERGE_MAX_WORKERS = 1024;
-
-// Rows that a block joins at a time, by the item's parts: see few() and the
-// spread below.
-__device__ __forceinline__ int merge_job_rows(int parts)
-{
-    return parts <= 2 ? 32 : parts <= 4 ? 16 : parts <= 8 ? 8 : parts < 16 ? 4 : parts < 32 ? 2 : 1;
-}
-
 struct MergeParams {
     paged::Parts parts;
     uint16_t *y;
@@ -577,180 +588,146 @@ struct Merge {
 };
 
 template <int D>
-__global__ void __launch_bounds__(MERGE_THREADS) merge_kernel(const MergeParams p)
+__global__ void __launch_bounds__(MERGE_THREADS, 2) merge_kernel(const MergeParams p)
 {
     using M = Merge<D>;
-    constexpr int PER = MERGE_MAX_WORKERS / MERGE_THREADS;
     __shared__ float partial[MERGE_WARPS][D];
-    __shared__ uint32_t ends[MERGE_MAX_WORKERS / 32];  // first slots that end an item (or hold none)
-    __shared__ int begin[MERGE_MAX_WORKERS];           // first job of the item that starts there
-    __shared__ int16_t count[MERGE_MAX_WORKERS];       // its parts
-    __shared__ uint32_t empty[MERGE_MAX_WORKERS / 32]; // first slots that hold none
-    __shared__ int warp_jobs[MERGE_WARPS];
+    __shared__ paged::PartHeader begun[MERGE_WARPS];
+    __shared__ int count[MERGE_WARPS];                 // parts; 0: no split item begins there
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // PER consecutive workers a thread
-    const int w0 = threadIdx.x * PER;
-    int2 cont[PER], start[PER];                        // {rows, more} of the workers' two slots
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        cont[i] = start[i] = make_int2(0, 0);
-        if (w0 + i < p.workers) {
-            cont[i] = *reinterpret_cast<const int2 *>(p.parts.headers + 2 * (w0 + i));
-            start[i] = *reinterpret_cast<const int2 *>(p.parts.headers + 2 * (w0 + i) + 1);
-        }
-    }
-    uint32_t stop = 0, none = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        stop |= (cont[i].x == 0 || cont[i].y == 0 ? 1u : 0u) << i;
-        none |= (cont[i].x == 0 ? 1u : 0u) << i;
-    }
-    static_assert(PER == 4, "a warp's lanes hold four words' bits of 32 workers");
-    stop <<= 4 * (lane & 7);
-    none <<= 4 * (lane & 7);
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) {
-        stop |= __shfl_xor_sync(0xffffffffu, stop, o);
-        none |= __shfl_xor_sync(0xffffffffu, none, o);
-    }
-    if ((lane & 7) == 0) {
-        ends[threadIdx.x >> 3] = stop;
-        empty[threadIdx.x >> 3] = none;
-    }
-    __syncthreads();
-    int jobs_of[PER], jobs = 0;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        jobs_of[i] = 0;
-        if (start[i].x > 0 && start[i].x <= p.parts.row_cap && start[i].y != 0) {
-            // the next worker behind w0 + i whose first slot ends an item
-            int at = w0 + i + 1;
-            uint32_t bits = at < MERGE_MAX_WORKERS ? ends[at >> 5] >> (at & 31) : 1u;
-            while (bits == 0) {
-                at = (at | 31) + 1;
-                bits = at < MERGE_MAX_WORKERS ? ends[at >> 5] : 1u;
+    {
+        const int wk = blockIdx.x * MERGE_WARPS + warp;
+        paged::PartHeader hd{};
+        if (wk < p.workers)
+            hd = p.parts.headers[2 * wk + 1];
+        int n = 1;
+        // the following workers' first slots, 32 at a time, up to the last part
+        for (int at = wk + 1;; at += 32) {
+            paged::PartHeader next{};
+            if (at + lane < p.workers)
+                next = p.parts.headers[2 * (at + lane)];
+            if (hd.rows == 0 || !hd.more) {
+                n = 0;
+                break;
             }
-            at += __ffs(bits) - 1;
+            const unsigned ends = __ballot_sync(0xffffffffu, next.rows == 0 || !next.more);
+            if (ends == 0) {
+                n += 32;
+                continue;
+            }
+            const int last = __ffs(ends) - 1;
             // (an item whose last part is missing, as a worker gave up, is left out)
-            if (at < MERGE_MAX_WORKERS && ((empty[at >> 5] >> (at & 31)) & 1u) == 0) {
-                const int n = at - (w0 + i) + 1;
-                count[w0 + i] = static_cast<int16_t>(n);
-                const int job = merge_job_rows(n);
-                jobs_of[i] = (start[i].x + job - 1) / job;
+            n = __shfl_sync(0xffffffffu, next.rows, last) == 0 ? 0 : n + last + 1;
+            break;
+        }
+        if (n > 0) {
+            // a workspace that another call writes at the same time (which is not
+            // allowed) may hold anything: no address comes from it unchecked
+            const int64_t last =
+                static_cast<int64_t>(hd.hm / p.work.kv_heads) * p.work.item_rows + hd.rows - 1;
+            if (hd.rows < 0 || hd.rows > p.parts.row_cap || hd.hm < 0 || hd.row < 0 ||
+                last >= (int64_t(1) << 31) ||
+                hd.row + static_cast<int64_t>(p.work.by_group(static_cast<int>(last))) >=
+                    p.work.seqs.tokens) {
+                paged::fault_index();
+                n = 0;
             }
         }
-        jobs += jobs_of[i];
-    }
-    int upto = jobs;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, upto, o);
-        if (lane >= o)
-            upto += x;
-    }
-    if (lane == 31)
-        warp_jobs[warp] = upto;
-    __syncthreads();
-    int total = 0;
-#pragma unroll
-    for (int k = 0; k < MERGE_WARPS; ++k) {
-        upto += k < warp ? warp_jobs[k] : 0;
-        total += warp_jobs[k];
-    }
-    upto -= jobs;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        begin[w0 + i] = upto;
-        upto += jobs_of[i];
+        if (lane == 0) {
+            begun[warp] = hd;
+            count[warp] = n;
+        }
     }
     __syncthreads();
-
-    for (int job = blockIdx.x; job < total; job += gridDim.x) {
-        // the last worker whose first job is at most this one
-        int wk = 0;
-#pragma unroll
-        for (int step = MERGE_MAX_WORKERS / 2; step > 0; step >>= 1)
-            if (begin[wk + step] <= job)
-                wk += step;
-        M mg{p, p.parts.headers[2 * wk + 1], 2 * wk + 1, count[wk], lane, 0};
+    // the items of few parts: groups of their rows, dealt to all warps
+    for (int j = blockIdx.y * MERGE_WARPS + warp;; j += gridDim.y * MERGE_WARPS) {
+        int i = 0, g = j, parts = 0;
+        for (; i < MERGE_WARPS; ++i) {
+            parts = count[i];
+            const int group = parts <= 2 ? 4 : parts <= 4 ? 2 : 1;
+            const int groups = parts == 0 || parts > 8 ? 0 : (begun[i].rows + group - 1) / group;
+            if (g < groups)
+                break;
+            g -= groups;
+        }
+        if (i == MERGE_WARPS)
+            break;
+        M mg{p, begun[i], 2 * (static_cast<int>(blockIdx.x) * MERGE_WARPS + i) + 1, parts, lane, 0};
         mg.m = mg.hd.hm / p.work.kv_heads;
-        const int rows = mg.hd.rows, parts = mg.parts;
-        // a workspace that another call writes at the same time (which is not
-        // allowed) may hold anything: no address comes from it unchecked
-        const int64_t last = static_cast<int64_t>(mg.m) * p.work.item_rows + rows - 1;
-        if (rows < 0 || rows > p.parts.row_cap || mg.hd.hm < 0 || mg.hd.row < 0 ||
-            last >= (int64_t(1) << 31) ||
-            mg.hd.row + static_cast<int64_t>(p.work.by_group(static_cast<int>(last))) >=
-                p.work.seqs.tokens) {
-            paged::fault_index();
-            return;
-        }
-        const int r0 = (job - begin[wk]) * merge_job_rows(parts);
-        if (parts <= 8) {
-            if (parts <= 2)
-                mg.template few<2>(r0 + 4 * warp);
-            else if (parts <= 4)
-                mg.template few<4>(r0 + 2 * warp);
-            else
-                mg.template few<8>(r0 + warp);
+        if (parts <= 2)
+            mg.template few<2>(g * 4);
+        else if (parts <= 4)
+            mg.template few<4>(g * 2);
+        else
+            mg.template few<8>(g);
+    }
+    // the others: a row's parts spread over the block
+    for (int i = 0; i < MERGE_WARPS; ++i) {
+        const int parts = count[i];
+        if (parts <= 8)
             continue;
-        }
+        M mg{p, begun[i], 2 * (static_cast<int>(blockIdx.x) * MERGE_WARPS + i) + 1, parts, lane, 0};
+        mg.m = mg.hd.hm / p.work.kv_heads;
+        const int rows = mg.hd.rows;
         // warps a row: as many as leave each about four parts
         const int spread = parts >= 32 ? 8 : parts >= 16 ? 4 : 2;
         const int sub = warp & (spread - 1);
-        const int r = r0 + warp / spread;
-        const bool live = r < rows;
-        float2 ml = make_float2(-INFINITY, 0.0f);
-        float top = -INFINITY;
-        for (int i = lane; live && i < parts; i += 32) {
-            ml = p.parts.ml[mg.at(i, r)];
-            top = fmaxf(top, ml.x);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float base = top == -INFINITY ? 0.0f : top;
-        float l = 0.0f;
-        float acc[M::VEC] = {};
-        for (int i0 = 0; i0 < parts; i0 += 32) {
-            float f = 0.0f;
-            if (live && i0 + lane < parts) {
-                if (parts > 32)
-                    ml = p.parts.ml[mg.at(i0 + lane, r)];
-                f = exp2_approx(ml.x - base);
-                l = fmaf(ml.y, f, l);
+        const int pass = MERGE_WARPS / spread;         // rows of the block at a time
+        for (int r0 = blockIdx.y * pass; r0 < rows; r0 += gridDim.y * pass) {
+            const int r = r0 + warp / spread;
+            const bool live = r < rows;
+            float2 ml = make_float2(-INFINITY, 0.0f);
+            float top = -INFINITY;
+            for (int i = lane; live && i < parts; i += 32) {
+                ml = p.parts.ml[mg.at(i, r)];
+                top = fmaxf(top, ml.x);
             }
-            const int n = min(32, parts - i0);
-            for (int b = sub; b < n; b += 8 * spread) {
-                typename M::Vec x[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (live && b + k * spread < n)
-                        x[k] = mg.load(i0 + b + k * spread, r);
+            for (int o = 16; o > 0; o >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            const float base = top == -INFINITY ? 0.0f : top;
+            float l = 0.0f;
+            float acc[M::VEC] = {};
+            for (int i0 = 0; i0 < parts; i0 += 32) {
+                float f = 0.0f;
+                if (live && i0 + lane < parts) {
+                    if (parts > 32)
+                        ml = p.parts.ml[mg.at(i0 + lane, r)];
+                    f = exp2_approx(ml.x - base);
+                    l = fmaf(ml.y, f, l);
+                }
+                const int n = min(32, parts - i0);
+                for (int b = sub; b < n; b += 8 * spread) {
+                    typename M::Vec x[8];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float g = __shfl_sync(0xffffffffu, f, (b + k * spread) & 31);
-                    if (live && b + k * spread < n)
-                        M::add(acc, x[k], g);
+                    for (int k = 0; k < 8; ++k)
+                        if (live && b + k * spread < n)
+                            x[k] = mg.load(i0 + b + k * spread, r);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float g = __shfl_sync(0xffffffffu, f, (b + k * spread) & 31);
+                        if (live && b + k * spread < n)
+                            M::add(acc, x[k], g);
+                    }
                 }
             }
-        }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            l += __shfl_xor_sync(0xffffffffu, l, o);
-        __syncthreads();                               // the previous job's sums have been read
+            for (int o = 16; o > 0; o >>= 1)
+                l += __shfl_xor_sync(0xffffffffu, l, o);
+            __syncthreads();                               // the sums before have been read
 #pragma unroll
-        for (int c = 0; c < M::VEC; ++c)
-            partial[warp][M::VEC * lane + c] = acc[c];
-        __syncthreads();
-        if (live && sub == 0) {
-            for (int k = 1; k < spread; ++k)
+            for (int c = 0; c < M::VEC; ++c)
+                partial[warp][M::VEC * lane + c] = acc[c];
+            __syncthreads();
+            if (live && sub == 0) {
+                for (int k = 1; k < spread; ++k)
 #pragma unroll
-                for (int c = 0; c < M::VEC; ++c)
-                    acc[c] += partial[warp + k][M::VEC * lane + c];
-            mg.store(r, acc, top, l);
+                    for (int c = 0; c < M::VEC; ++c)
+                        acc[c] += partial[warp + k][M::VEC * lane + c];
+                mg.store(r, acc, top, l);
+            }
         }
     }
 }
