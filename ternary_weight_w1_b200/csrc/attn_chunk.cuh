@@ -20,6 +20,17 @@
 // step's chain of loads, maxima, exponentials and stores took 1850 clocks: two
 // warps a scheduler do not hide their latencies.)
 //
+// Items that are split into up to four parts, as most split ones are, are joined
+// here: a worker computes the part of the item that began before its run first
+// and raises a flag per warp behind it; the item's first worker comes to its
+// part last, finds the flags of the same warp (same rows, same channels) and
+// adds the parts to its own, in the order of the keys, before it writes the
+// output. The flags hold the launch's number, so their memory needs no
+// initialisation; the kernel behind this one, which joins items of more parts,
+// clears them. Blocks wait only for blocks of a higher number, which are never
+// kept from running by them. (Leaving every part to a kernel of its own took
+// 18 us of 60 at 2048 tokens of the 2B layer.)
+//
 // One persistent block per SM. Warps 0-7 and 8-15 compute the halves' softmax,
 // warp 16 fetches keys and values through a ring of tiles, warps 17 and 18
 // issue the products of one half each, warp 19 fetches the next item's queries
@@ -40,6 +51,41 @@ constexpr int STEP = 64;               // keys of a step: the tile's two halves
 constexpr int SOFTMAX_WARPS = 16;
 constexpr int THREADS = (SOFTMAX_WARPS + 4) * 32;
 constexpr int TMEM_COLS = 512;
+constexpr int JOIN = 3;                // parts behind its own that a worker joins
+__device__ __forceinline__ uint64_t ld_acquire_u64(const uint64_t *p)
+{
+    uint64_t v;
+    asm volatile("ld.acquire.gpu.global.b64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void st_release_u64(uint64_t *p, uint64_t v)
+{
+    asm volatile("st.release.gpu.global.b64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
+}
+
+// Waits until the flag is nonce or nonce + 1 and returns it; 0 after the limit,
+// or when the block gives up.
+__device__ __forceinline__ uint64_t wait_flag(const uint64_t *flag, uint64_t nonce,
+                                              volatile int *abort, uint64_t limit_ns)
+{
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t spin = 0;; ++spin) {
+        const uint64_t v = ld_acquire_u64(flag);
+        if ((v & ~uint64_t(1)) == nonce)
+            return v;
+        if ((spin & 63u) == 63u) {
+            if (*abort)
+                return 0;
+            if (global_timer_ns() - t0 > limit_ns) {
+                atomicOr(&g_fault_word, FAULT_WAIT_TIMEOUT);
+                *abort = 1;
+                return 0;
+            }
+        }
+    }
+}
+
 template <int D>
 struct Cfg {
     static constexpr int CH = D / 64;                          // 64-channel column blocks
@@ -626,62 +672,158 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tc_fence_after_sync();
             }
             if (active && !idle) {
-                const float f = whole ? inv_sum(l) : 1.0f;
-                const int64_t slot_row = static_cast<int64_t>(slot) * p.parts.row_cap;
-                // This warp's half of the channels, 64 bytes of each row at a
-                // time through its staging rows, from where four lanes write a
-                // row's 64 bytes.
-                char *dst[4];                                  // of the rows that this lane writes
+                const int64_t slot_row = static_cast<int64_t>(slot) * p.parts.row_cap + r;
+                bool final = whole;
+                float f = 1.0f, fk[JOIN];                      // factors of the parts
+                int others = 0;                                // that are joined here
+                const float4 *const o_parts =
+                    reinterpret_cast<const float4 *>(p.parts.o) +
+                    static_cast<int64_t>(part * (D / 8)) * p.parts.row_cap + r;
+                const int64_t slot_o = static_cast<int64_t>(p.parts.row_cap) * (D / 4);
+                if (from_start && !to_end) {
+                    uint64_t flag = 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int at = r - lane + i * 8 + (lane >> 2);
-                    dst[i] = whole ? reinterpret_cast<char *>(p.y + row_of(cur, at, p.y_stride) +
-                                                              part * (D / 2))
-                                   : reinterpret_cast<char *>(p.parts.o + (slot_row + at) * D +
-                                                              part * (D / 2));
-                    dst[i] = at < end ? dst[i] + (lane & 3) * 16 : nullptr;
+                    for (int k = 0; k < JOIN; ++k) {
+                        if (final)
+                            break;
+                        if (lane == 0)
+                            flag = wait_flag(p.parts.flags + (worker + 1 + k) * 16 + warp, p.nonce,
+                                             abort_flag, p.wait_limit_ns);
+                        flag = __shfl_sync(0xffffffffu, flag, 0);
+                        ok = named_bar_and(pair_bar, 64, flag != 0);
+                        if (!ok)
+                            break;
+                        others = k + 1;
+                        final = flag == p.nonce;               // this part ends the item
+                    }
+                    if (!ok)
+                        break;
+                    if (!final)
+                        others = 0;                            // too many: left to the next kernel
                 }
-                uint4 *const mine = reinterpret_cast<uint4 *>(out + lane * 64);
-                const int chunks = whole ? D / 64 : D / 32;
+                if (others > 0) {
+                    head[1].rows = 0;                          // nothing is left to merge
+                    float2 ml[JOIN];
+                    float top = m;
+#pragma unroll
+                    for (int k = 0; k < JOIN; ++k) {
+                        ml[k] = make_float2(-INFINITY, 0.0f);
+                        if (k < others && r < end)
+                            ml[k] = __ldcg(p.parts.ml +
+                                           static_cast<int64_t>(2 * (worker + 1 + k)) *
+                                               p.parts.row_cap + r);
+                        top = fmaxf(top, ml[k].x);
+                    }
+                    const float base = top == -INFINITY ? 0.0f : top;
+                    f = exp2_approx(m - base);
+                    l *= f;
+                    m = top;
+#pragma unroll
+                    for (int k = 0; k < JOIN; ++k) {
+                        fk[k] = exp2_approx(ml[k].x - base);
+                        l = fmaf(ml[k].y, fk[k], l);
+                    }
+                }
+                if (final) {
+                    // This warp's half of the channels, 64 bytes of each row at a
+                    // time through its staging rows, from where four lanes write a
+                    // row's 64 bytes.
+                    const float inv = inv_sum(l);
+                    f *= inv;
+                    char *dst[4];                              // of the rows that this lane writes
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int at = r - lane + i * 8 + (lane >> 2);
+                        dst[i] = at < end ? reinterpret_cast<char *>(
+                                                p.y + row_of(cur, at, p.y_stride) + part * (D / 2)) +
+                                                (lane & 3) * 16
+                                          : nullptr;
+                    }
+                    uint4 *const mine = reinterpret_cast<uint4 *>(out + lane * 64);
 #pragma unroll 1
-                for (int c = 0; c < chunks; ++c) {
-                    uint32_t x[16];
-                    if (whole) {
-                        uint32_t o[32];
+                    for (int c = 0; c < D / 64; ++c) {
+                        uint32_t x[16], o[32];
                         tmem_ld_32x32b_x32(o_addr + c * 32, o);
                         tmem_ld_wait();
                         loaded32(o);
 #pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+#pragma unroll
+                        for (int k = 0; k < JOIN; ++k) {
+                            if (k >= others)
+                                break;
+                            const float4 *src = o_parts + 2 * (worker + 1 + k) * slot_o;
+                            const float g = fk[k] * inv;
+                            float4 v[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                v[i] = r < end ? __ldcg(src + (c * 8 + i) * p.parts.row_cap)
+                                               : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float e[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    o[4 * i + q] = __float_as_uint(
+                                        fmaf(e[q], g, __uint_as_float(o[4 * i + q])));
+                            }
+                        }
+#pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            x[i] = pack_bf16(__uint_as_float(o[2 * i]) * f,
-                                             __uint_as_float(o[2 * i + 1]) * f);
-                    } else {
-                        tmem_ld_x16(o_addr + c * 16, x);
+                            x[i] = pack_bf16(__uint_as_float(o[2 * i]),
+                                             __uint_as_float(o[2 * i + 1]));
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            mine[i ^ ((lane >> 1) & 3)] =
+                                make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                        __syncwarp();
+                        uint4 v[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int at = i * 8 + (lane >> 2);        // row of the warp
+                            v[i] = reinterpret_cast<const uint4 *>(
+                                out + at * 64)[(lane & 3) ^ ((at >> 1) & 3)];
+                        }
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (dst[i] != nullptr)
+                                *reinterpret_cast<uint4 *>(dst[i] + c * 64) = v[i];
+                        __syncwarp();
                     }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        mine[i ^ ((lane >> 1) & 3)] =
-                            make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-                    __syncwarp();
-                    uint4 v[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int at = i * 8 + (lane >> 2);            // row of the warp
-                        v[i] = reinterpret_cast<const uint4 *>(
-                            out + at * 64)[(lane & 3) ^ ((at >> 1) & 3)];
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (dst[i] != nullptr)
-                            *reinterpret_cast<uint4 *>(dst[i] + c * 64) = v[i];
-                    __syncwarp();
-                }
-                if (r < end && part == 0) {
-                    if (!whole)
-                        p.parts.ml[slot_row + r] = make_float2(m, l);
-                    else if (p.lse != nullptr)
+                    if (r < end && part == 0 && p.lse != nullptr)
                         p.lse[(cur.v.q0 + tok) * static_cast<int64_t>(p.q_heads) +
                               cur.h * w.group + rr - tok * w.group] = lse_of(m, l);
+                } else {
+                    float4 *mine = reinterpret_cast<float4 *>(
+                                       p.parts.o + static_cast<int64_t>(slot) * p.parts.row_cap * D) +
+                                   static_cast<int64_t>(part * (D / 8)) * p.parts.row_cap + r;
+#pragma unroll 1
+                    for (int c = 0; c < D / 64; ++c) {
+                        uint32_t o[32];
+                        tmem_ld_32x32b_x32(o_addr + c * 32, o);
+                        tmem_ld_wait();
+                        loaded32(o);
+                        if (r < end) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                mine[(c * 8 + i) * p.parts.row_cap] = make_float4(
+                                    __uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                    __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                        }
+                    }
+                    if (r < end && part == 0)
+                        p.parts.ml[slot_row] = make_float2(m, l);
+                    if (!from_start) {
+                        // either warp's flag also stands for m and l, which one of
+                        // them has written
+                        __threadfence();
+                        __syncwarp();
+                        named_bar_and(pair_bar, 64, true);
+                        if (lane == 0)
+                            st_release_u64(p.parts.flags + worker * 16 + warp,
+                                           p.nonce + (to_end ? 0 : 1));
+                    }
                 }
             }
             left -= nt;
@@ -739,6 +881,80 @@ __global__ void __launch_bounds__(THREADS, 1)
             head[0].rows = head[1].rows = 0;
         p.parts.headers[2 * worker] = head[0];
         p.parts.headers[2 * worker + 1] = head[1];
+    }
+}
+
+// Joins the items of more parts than that (one sequence's long context shared
+// by many workers) and clears the flags. A warp takes 32 rows, one a lane, and
+// four channels, of which every part is one whole line.
+template <int D>
+__global__ void __launch_bounds__(MERGE_THREADS) join_kernel(const MergeParams p)
+{
+    __shared__ paged::PartHeader begun[MERGE_WARPS];
+    __shared__ int count[MERGE_WARPS];
+    pdl_wait();
+    pdl_launch_dependents();
+    // (a captured launch raises the same flags every time it is replayed)
+    for (int i = (blockIdx.y * gridDim.x + blockIdx.x) * MERGE_THREADS + threadIdx.x;
+         i < 16 * p.workers; i += gridDim.x * gridDim.y * MERGE_THREADS)
+        p.parts.flags[i] = 0;
+    list_items(p, begun, count);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row_cap = p.parts.row_cap;
+    for (int i = 0; i < MERGE_WARPS; ++i) {
+        const int parts = count[i];
+        if (parts == 0)
+            continue;
+        const paged::PartHeader hd = begun[i];
+        const int first = 2 * (static_cast<int>(blockIdx.x) * MERGE_WARPS + i) + 1;
+        const int m = hd.hm / p.work.kv_heads;
+        const int units = (hd.rows + 31) / 32 * (D / 4);
+        for (int u = blockIdx.y * MERGE_WARPS + warp; u < units; u += gridDim.y * MERGE_WARPS) {
+            const int r = u / (D / 4) * 32 + lane, c4 = u % (D / 4);
+            if (r >= hd.rows)
+                continue;
+            // part 0 is slot `first`, part k > 0 slot first + 2 k - 1
+            auto slot = [&](int k) {
+                return static_cast<int64_t>(first + (k > 0 ? 2 * k - 1 : 0)) * row_cap;
+            };
+            float top = -INFINITY;
+#pragma unroll 8
+            for (int k = 0; k < parts; ++k)
+                top = fmaxf(top, p.parts.ml[slot(k) + r].x);
+            const float base = top == -INFINITY ? 0.0f : top;
+            float l = 0.0f;
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int k0 = 0; k0 < parts; k0 += 8) {
+                float2 ml[8];
+                float4 v[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k0 + k < parts) {
+                        ml[k] = p.parts.ml[slot(k0 + k) + r];
+                        v[k] = reinterpret_cast<const float4 *>(
+                            p.parts.o)[slot(k0 + k) * (D / 4) + static_cast<int64_t>(c4) * row_cap + r];
+                    }
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k0 + k < parts) {
+                        const float f = exp2_approx(ml[k].x - base);
+                        l = fmaf(ml[k].y, f, l);
+                        o.x = fmaf(v[k].x, f, o.x);
+                        o.y = fmaf(v[k].y, f, o.y);
+                        o.z = fmaf(v[k].z, f, o.z);
+                        o.w = fmaf(v[k].w, f, o.w);
+                    }
+            }
+            const int rr = m * p.work.item_rows + r;
+            const int tok = p.work.by_group(rr);
+            const int hq = (hd.hm - m * p.work.kv_heads) * p.work.group + rr - tok * p.work.group;
+            const int64_t row = hd.row + tok;
+            const float f = inv_sum(l);
+            *reinterpret_cast<uint2 *>(p.y + row * p.y_stride + hq * D + 4 * c4) =
+                make_uint2(pack_bf16(o.x * f, o.y * f), pack_bf16(o.z * f, o.w * f));
+            if (p.lse != nullptr && c4 == 0)
+                p.lse[row * p.q_heads + hq] = lse_of(top, l);
+        }
     }
 }
 

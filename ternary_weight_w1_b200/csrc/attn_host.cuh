@@ -145,19 +145,21 @@ bool make_map_q(CUtensorMap *map, const attn::Params &p, int64_t head_dim, int t
 
 // The parts of one attention kernel inside the workspace: headers, maxima and
 // sums, accumulators, for two slots a worker.
-size_t parts_layout(int64_t workers, int64_t row_cap, int64_t head_dim, char *base,
+size_t parts_layout(int64_t workers, int64_t row_cap, int64_t head_dim, bool flags, char *base,
                     paged::Parts *out)
 {
     const size_t hb = round_up(static_cast<size_t>(2 * workers) * sizeof(paged::PartHeader), 256);
     const size_t mb = round_up(static_cast<size_t>(2 * workers * row_cap) * sizeof(float2), 256);
     const size_t ob = round_up(static_cast<size_t>(2 * workers * row_cap * head_dim) * 4, 256);
+    const size_t fb = flags ? round_up(static_cast<size_t>(16 * workers) * sizeof(uint64_t), 256) : 0;
     if (out != nullptr) {
         out->headers = reinterpret_cast<paged::PartHeader *>(base);
         out->ml = reinterpret_cast<float2 *>(base + hb);
         out->o = reinterpret_cast<float *>(base + hb + mb);
+        out->flags = flags ? reinterpret_cast<uint64_t *>(base + hb + mb + ob) : nullptr;
         out->row_cap = static_cast<int>(row_cap);
     }
-    return hb + mb + ob;
+    return hb + mb + ob + fb;
 }
 
 constexpr int kRowsKernelMax = 32;                   // rows of the rows kernel's largest item
@@ -174,14 +176,15 @@ AttnLayout attn_layout(int64_t rows, int64_t head_dim, char *base)
     AttnLayout l{};
     const int blocks = head_dim == 64 ? attn::rows::Cfg<64>::BLOCKS : attn::rows::Cfg<128>::BLOCKS;
     l.bytes = parts_layout(kAttnMaxGrid * blocks * attn::rows::WARPS,
-                           std::min<int64_t>(rows, kRowsKernelMax), head_dim, base, &l.rows);
+                           std::min<int64_t>(rows, kRowsKernelMax), head_dim, false, base, &l.rows);
     if (rows > kRowsKernelMax)
         l.bytes += parts_layout(kAttnMaxGrid, std::min<int64_t>(rows, 2 * attn::chunk::HALF), head_dim,
-                                base + l.bytes, &l.chunk);
+                                true, base + l.bytes, &l.chunk);
     return l;
 }
 
-int launch_merge(const attn::Params &p, int64_t head_dim, int workers, const DeviceInfo &dev,
+template <int D>
+int launch_merge(const attn::Params &p, int workers, bool chunk, const DeviceInfo &dev,
                  cudaStream_t st)
 {
     const attn::MergeParams m{p.parts, p.y, p.y_stride, p.lse, p.q_heads, p.work, workers};
@@ -189,8 +192,8 @@ int launch_merge(const attn::Params &p, int64_t head_dim, int workers, const Dev
     const int x = (workers + attn::MERGE_WARPS - 1) / attn::MERGE_WARPS;
     const int rows = std::min(p.work.item_rows, p.parts.row_cap);
     const dim3 grid(x, std::max(1, std::min(rows, 2 * dev.sms / x))), block(attn::MERGE_THREADS);
-    return launch_status(head_dim == 64 ? launch(attn::merge_kernel<64>, grid, block, 0, st, m)
-                                        : launch(attn::merge_kernel<128>, grid, block, 0, st, m));
+    return launch_status(launch(chunk ? attn::chunk::join_kernel<D> : attn::merge_kernel<D>, grid,
+                                block, 0, st, m));
 }
 
 template <int D, int MT>
@@ -210,7 +213,18 @@ int run_attn_rows(attn::Params p, const bitlinear_kv_cache &cache, const DeviceI
         e = launch(attn::rows::attn_rows_kernel<D, MT>, dim3(grid), dim3(attn::rows::THREADS),
                    static_cast<size_t>(smem), st, maps, p);
     const int rc = launch_status(e);
-    return rc != BITLINEAR_OK ? rc : launch_merge(p, D, grid * attn::rows::WARPS, dev, st);
+    return rc != BITLINEAR_OK ? rc : launch_merge<D>(p, grid * attn::rows::WARPS, false, dev, st);
+}
+
+// A number for every launch of the chunk kernel in this process: even, and
+// counted from a place that no other memory content is likely to hold (the time
+// of the first launch, spread over 64 bits by a multiplication).
+uint64_t next_nonce()
+{
+    static std::atomic<uint64_t> next{
+        static_cast<uint64_t>(std::chrono::system_clock::now().time_since_epoch().count()) *
+            0x9E3779B97F4A7C15ull & ~uint64_t(1)};
+    return next.fetch_add(2);
 }
 
 template <int D>
@@ -234,7 +248,7 @@ int run_attn_chunk(attn::Params p, const bitlinear_kv_cache &cache, const Device
         e = launch(attn::chunk::attn_chunk_kernel<D>, dim3(grid), dim3(attn::chunk::THREADS),
                    static_cast<size_t>(smem), st, maps, q_map, p);
     const int rc = launch_status(e);
-    return rc != BITLINEAR_OK ? rc : launch_merge(p, D, grid, dev, st);
+    return rc != BITLINEAR_OK ? rc : launch_merge<D>(p, grid, true, dev, st);
 }
 
 // The kernels of a step, by the rows (new tokens times query heads per key
@@ -268,6 +282,7 @@ int run_attention(attn::Params p, const bitlinear_kv_cache &cache, int64_t max_r
         p.work.max_rows = INT_MAX;
     }
     p.parts = layout.chunk;
+    p.nonce = next_nonce();
     return run_attn_chunk<D>(p, cache, dev, st);
 }
 

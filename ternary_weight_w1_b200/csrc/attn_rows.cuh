@@ -72,6 +72,7 @@ struct Params {
     paged::Work work;
     paged::Parts parts;
     uint64_t wait_limit_ns;
+    uint64_t nonce;            // even, another for every launch
 };
 
 struct Maps {
@@ -587,60 +588,67 @@ struct Merge {
     }
 };
 
+// Lists the split items that begin in workers 8 x .. 8 x + 7, one a warp: their
+// headers and numbers of parts (0: none begins there). Ends with a barrier.
+__device__ __forceinline__ void list_items(const MergeParams &p, paged::PartHeader *begun,
+                                           int *count)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int wk = blockIdx.x * MERGE_WARPS + warp;
+    paged::PartHeader hd{};
+    if (wk < p.workers)
+        hd = p.parts.headers[2 * wk + 1];
+    int n = 1;
+    // the following workers' first slots, 32 at a time, up to the last part
+    for (int at = wk + 1;; at += 32) {
+        paged::PartHeader next{};
+        if (at + lane < p.workers)
+            next = p.parts.headers[2 * (at + lane)];
+        if (hd.rows == 0 || !hd.more) {
+            n = 0;
+            break;
+        }
+        const unsigned ends = __ballot_sync(0xffffffffu, next.rows == 0 || !next.more);
+        if (ends == 0) {
+            n += 32;
+            continue;
+        }
+        const int last = __ffs(ends) - 1;
+        // (an item whose last part is missing, as a worker gave up, is left out)
+        n = __shfl_sync(0xffffffffu, next.rows, last) == 0 ? 0 : n + last + 1;
+        break;
+    }
+    if (n > 0) {
+        // a workspace that another call writes at the same time (which is not
+        // allowed) may hold anything: no address comes from it unchecked
+        const int64_t last =
+            static_cast<int64_t>(hd.hm / p.work.kv_heads) * p.work.item_rows + hd.rows - 1;
+        if (hd.rows < 0 || hd.rows > p.parts.row_cap || hd.hm < 0 || hd.row < 0 ||
+            last >= (int64_t(1) << 31) ||
+            hd.row + static_cast<int64_t>(p.work.by_group(static_cast<int>(last))) >=
+                p.work.seqs.tokens) {
+            paged::fault_index();
+            n = 0;
+        }
+    }
+    if (lane == 0) {
+        begun[warp] = hd;
+        count[warp] = n;
+    }
+    __syncthreads();
+}
+
 template <int D>
 __global__ void __launch_bounds__(MERGE_THREADS, 2) merge_kernel(const MergeParams p)
 {
     using M = Merge<D>;
     __shared__ float partial[MERGE_WARPS][D];
     __shared__ paged::PartHeader begun[MERGE_WARPS];
-    __shared__ int count[MERGE_WARPS];                 // parts; 0: no split item begins there
+    __shared__ int count[MERGE_WARPS];
     pdl_wait();
     pdl_launch_dependents();
+    list_items(p, begun, count);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    {
-        const int wk = blockIdx.x * MERGE_WARPS + warp;
-        paged::PartHeader hd{};
-        if (wk < p.workers)
-            hd = p.parts.headers[2 * wk + 1];
-        int n = 1;
-        // the following workers' first slots, 32 at a time, up to the last part
-        for (int at = wk + 1;; at += 32) {
-            paged::PartHeader next{};
-            if (at + lane < p.workers)
-                next = p.parts.headers[2 * (at + lane)];
-            if (hd.rows == 0 || !hd.more) {
-                n = 0;
-                break;
-            }
-            const unsigned ends = __ballot_sync(0xffffffffu, next.rows == 0 || !next.more);
-            if (ends == 0) {
-                n += 32;
-                continue;
-            }
-            const int last = __ffs(ends) - 1;
-            // (an item whose last part is missing, as a worker gave up, is left out)
-            n = __shfl_sync(0xffffffffu, next.rows, last) == 0 ? 0 : n + last + 1;
-            break;
-        }
-        if (n > 0) {
-            // a workspace that another call writes at the same time (which is not
-            // allowed) may hold anything: no address comes from it unchecked
-            const int64_t last =
-                static_cast<int64_t>(hd.hm / p.work.kv_heads) * p.work.item_rows + hd.rows - 1;
-            if (hd.rows < 0 || hd.rows > p.parts.row_cap || hd.hm < 0 || hd.row < 0 ||
-                last >= (int64_t(1) << 31) ||
-                hd.row + static_cast<int64_t>(p.work.by_group(static_cast<int>(last))) >=
-                    p.work.seqs.tokens) {
-                paged::fault_index();
-                n = 0;
-            }
-        }
-        if (lane == 0) {
-            begun[warp] = hd;
-            count[warp] = n;
-        }
-    }
-    __syncthreads();
     // the items of few parts: groups of their rows, dealt to all warps
     for (int j = blockIdx.y * MERGE_WARPS + warp;; j += gridDim.y * MERGE_WARPS) {
         int i = 0, g = j, parts = 0;

@@ -321,7 +321,10 @@ struct PartHeader {
 struct Parts {
     PartHeader *headers;   // [2 * workers]
     float2 *ml;            // [2 * workers][row_cap]: maximum (log2 units) and sum
-    float *o;              // [2 * workers][row_cap][head_dim]
+    float *o;              // [2 * workers]: [row_cap][head_dim], or with flags
+                           // [head_dim / 4][row_cap][4], which a thread per row
+                           // writes and reads in whole lines
+    uint64_t *flags;       // [workers][16] or null: see the chunk kernel's output
     int row_cap;
 };
 
