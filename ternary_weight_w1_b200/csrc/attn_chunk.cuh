@@ -311,9 +311,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     // behind them.
     auto s_tmem = [&](int h, int b) { return tmem + h * 128 + b * STEP; };
     auto o_tmem = [&](int h) { return tmem + 256 + h * 128; };
+    // tiles of the item that begin in the `left` units of this run
     auto parts_tiles = [&](int64_t left) {
-        const int64_t n = cur.t.end - cur.tile;
-        return static_cast<int>(n < left ? n : left);
+        const int64_t n = cur.t.end - cur.tile, in_run = (left + cur.units - 1) / cur.units;
+        return static_cast<int>(n < in_run ? n : in_run);
     };
     const int half_rows = w.item_rows / 2;                     // whole tokens, at most HALF rows
     auto rows_of = [&]() { return min(w.item_rows, cur.v.qlen * w.group - cur.m * w.item_rows); };
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
             }
-            left -= nt;
+            left -= static_cast<int64_t>(nt) * cur.units;
             if (ok && left > 0)
                 cur.next_item(w);
         }
@@ -495,7 +496,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     next_stage();
                 }
             }
-            left -= nt;
+            left -= static_cast<int64_t>(nt) * cur.units;
             if (ok && left > 0)
                 cur.next_item(w);
         }
@@ -826,7 +827,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
             }
-            left -= nt;
+            left -= static_cast<int64_t>(nt) * cur.units;
             if (left > 0)
                 cur.next_item(w);
         }
@@ -858,7 +859,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 __syncwarp();
             }
-            left -= nt;
+            left -= static_cast<int64_t>(nt) * cur.units;
             if (left > 0)
                 cur.next_item(w);
         }

@@ -202,6 +202,7 @@ int run_attn_rows(attn::Params p, const bitlinear_kv_cache &cache, const DeviceI
 {
     constexpr int smem = attn::rows::Cfg<D>::SMEM_BYTES;
     p.work.item_rows = 16 * MT;
+    p.work.full = p.work.half = 1;
     attn::Maps maps{};
     const uint32_t box = static_cast<uint32_t>(std::min<int64_t>(cache.page, attn::rows::BN));
     if (!make_map_cache(&maps.k, cache.k_dev, cache, box) ||
@@ -234,6 +235,10 @@ int run_attn_chunk(attn::Params p, const bitlinear_kv_cache &cache, const Device
     constexpr int smem = attn::chunk::Cfg<D>::SMEM_BYTES;
     const int tokens = attn::chunk::HALF / p.work.group;       // of half an item
     p.work.item_rows = 2 * tokens * p.work.group;
+    // a tile takes 2.2 us with both halves at work, 1.3 us with one (measured,
+    // 128 channels)
+    p.work.full = 5;
+    p.work.half = 3;
     attn::Maps maps{};
     CUtensorMap q_map;
     if (!make_map_q(&q_map, p, D, tokens))

@@ -60,10 +60,11 @@ __device__ __forceinline__ int page_of(const Seqs &q, int s, int c)
 //
 // The attention's work is cut into items: item_rows consecutive rows of one
 // sequence and key head, where row r is query head r % group of token r / group, so the
-// query heads that share a key head share its tiles. An item takes one unit
-// per tile of BN keys that any of its rows sees. All units of a launch, items
-// in order and key heads outermost, are dealt to the workers in equal
-// contiguous runs: a long sequence is split wherever a run ends, and a batch
+// query heads that share a key head share its tiles. An item takes `full` units
+// per tile of BN keys that any of its rows sees, or `half` when it has no more
+// than half its rows. All units of a launch, items in order and key heads
+// outermost, are dealt to the workers in equal contiguous runs; a tile belongs to
+// the run that it begins in: a long sequence is split wherever a run ends, and a batch
 // of ragged ones stays balanced without the host knowing a length. A worker
 // that gets a whole item writes its output; otherwise it leaves a partial sum
 // that the merge kernel joins in the order of the keys.
@@ -87,6 +88,7 @@ struct Work {
     int group;             // query heads per key head
     int kv_heads;
     int item_rows;         // rows of an item
+    int full, half;        // units of a tile
     int window;            // 0: none
     int min_rows, max_rows;  // sequences of this launch: min_rows <= qlen * group <= max_rows
 };
@@ -153,6 +155,11 @@ __device__ __forceinline__ int64_t warp_scan(int64_t n)
     return n;
 }
 
+__device__ __forceinline__ int tile_units(const Work &w, const View &v, int m)
+{
+    return v.qlen * w.group - m * w.item_rows > w.item_rows / 2 ? w.full : w.half;
+}
+
 // Units of the 32 sequences of group g, one per lane (the whole warp). A
 // sequence of several items has them counted by all lanes.
 template <int BN>
@@ -170,7 +177,7 @@ __device__ __forceinline__ int64_t seq_units(const Work &w, int g)
     int64_t n = 0;
     if (v.qlen > 0 && !many) {
         const Tiles t = item_tiles<BN>(w, v, 0);
-        n = t.end - t.begin;
+        n = (t.end - t.begin) * tile_units(w, v, 0);
     }
     for (unsigned left = __ballot_sync(0xffffffffu, many); left != 0; left &= left - 1) {
         const int at = __ffs(left) - 1;
@@ -181,7 +188,7 @@ __device__ __forceinline__ int64_t seq_units(const Work &w, int g)
         int64_t sum = 0;
         for (int m = lane; m * w.item_rows < x.qlen * w.group; m += 32) {
             const Tiles t = item_tiles<BN>(w, x, m);
-            sum += t.end - t.begin;
+            sum += (t.end - t.begin) * tile_units(w, x, m);
         }
         sum = warp_sum(sum);
         if (lane == at)
@@ -190,10 +197,11 @@ __device__ __forceinline__ int64_t seq_units(const Work &w, int g)
     return n;
 }
 
-// A position in the launch's units: the item and the tile inside it.
+// A tile of the launch: the item and the tile inside it.
 template <int BN>
 struct Cursor {
     int h, s, k, m, tile;  // k-th item of the sequence: rows m * w.item_rows ..
+    int units;             // of each of its tiles
     View v;
     Tiles t;
 
@@ -201,10 +209,11 @@ struct Cursor {
     {
         m = item_at(k, items_of(w, v));
         t = item_tiles<BN>(w, v, m);
+        units = tile_units(w, v, m);
         tile = t.begin;
     }
 
-    // The first unit of the next item. Only called while units are left, so a
+    // The first tile of the next item. Only called while units are left, so a
     // sequence of this launch is always found.
     __device__ __forceinline__ void next_item(const Work &w)
     {
@@ -221,9 +230,11 @@ struct Cursor {
         open(w);
     }
 
-    // Moves to unit `off` of the 32 sequences of group g, whose units n the
-    // lanes hold (the whole warp).
-    __device__ __forceinline__ void seek(const Work &w, int g, int64_t n, int64_t off)
+    // Moves to the item that holds unit `off` of the 32 sequences of group g,
+    // whose units n the lanes hold (the whole warp), and to its first tile that
+    // begins there or behind. Returns how far behind; the tile may be the one
+    // after the item's last.
+    __device__ __forceinline__ int seek(const Work &w, int g, int64_t n, int64_t off)
     {
         const int lane = threadIdx.x & 31;
         const int64_t upto = warp_scan(n);
@@ -238,7 +249,7 @@ struct Cursor {
             int64_t c = 0;
             if (k0 + lane < items) {
                 const Tiles x = item_tiles<BN>(w, v, item_at(k0 + lane, items));
-                c = x.end - x.begin;
+                c = (x.end - x.begin) * tile_units(w, v, item_at(k0 + lane, items));
             }
             const int64_t sum = warp_scan(c);
             const unsigned in = __ballot_sync(0xffffffffu, off < sum);
@@ -251,7 +262,9 @@ struct Cursor {
             off -= __shfl_sync(0xffffffffu, sum, 31);
         }
         open(w);
-        tile = t.begin + static_cast<int>(off);
+        const int tiles = static_cast<int>((off + units - 1) / units);
+        tile = t.begin + tiles;
+        return static_cast<int>(static_cast<int64_t>(tiles) * units - off);
     }
 };
 
@@ -261,8 +274,9 @@ __device__ __forceinline__ int64_t quotient(int64_t n, int64_t d)
     return (n | d) >> 31 == 0 ? static_cast<uint32_t>(n) / static_cast<uint32_t>(d) : n / d;
 }
 
-// Deals the launch's units: the number that worker `worker` takes, with `cur`
-// at the first of them. Every warp of the block calls it (`workers` workers in
+// Deals the launch's units: those that worker `worker` has from the first tile
+// that begins in its run, where `cur` is set (none: 0). A run is never shorter
+// than a tile, so that an item's parts lie in successive workers. Every warp of the block calls it (`workers` workers in
 // all); `sums` is shared memory for MAX_GROUPS numbers that must not be used
 // for anything else until the block has met again. Up to 32 sequences every
 // warp counts by itself, without a barrier.
@@ -288,9 +302,13 @@ __device__ __forceinline__ int64_t deal(const Work &w, int worker, int workers, 
         per_head = warp_sum(per_head);
     }
     const int64_t units = per_head * w.kv_heads;
+    if (workers > units / w.full)
+        workers = static_cast<int>(max(units / w.full, static_cast<int64_t>(1)));
+    if (worker >= workers)
+        return 0;
     const int64_t base = quotient(units, workers);
     const int extra = static_cast<int>(units - base * workers);
-    const int64_t count = base + (worker < extra ? 1 : 0);
+    int64_t count = base + (worker < extra ? 1 : 0);
     if (count > 0) {
         const int64_t u = worker * base + min(worker, extra);
         cur.h = static_cast<int>(quotient(u, per_head));
@@ -301,9 +319,11 @@ __device__ __forceinline__ int64_t deal(const Work &w, int worker, int workers, 
                 off -= sums[g++];
             n = seq_units<BN>(w, g);
         }
-        cur.seek(w, g, n, off);
+        count -= cur.seek(w, g, n, off);
+        if (count > 0 && cur.tile == cur.t.end)
+            cur.next_item(w);
     }
-    return count;
+    return max(count, static_cast<int64_t>(0));
 }
 
 // Unnormalised sums of item parts, one slot per end of a worker's run:
