@@ -611,6 +611,54 @@ int bitlinear_paged_attention(const void *q_dev, int64_t q_stride,
                               void *workspace_dev, size_t workspace_bytes,
                               void *cuda_stream);
 
+/* One projection of bitlinear_attn_forward. */
+typedef struct {
+    const void *packed_dev;  /* packed weights (bitlinear_pack_weights) */
+    float gamma;
+    const float *gain_dev;   /* fp32 gains of its RMSNorm, 16-byte aligned, or NULL */
+} bitlinear_projection;
+
+/* Workspace bytes of bitlinear_attn_forward, whatever gains it is given;
+ * SIZE_MAX for shapes it refuses. */
+size_t bitlinear_workspace_bytes_attn(int64_t M, int64_t K, int64_t seqs,
+                                      int64_t q_heads, int64_t kv_heads,
+                                      int64_t head_dim);
+
+/* The attention block of a decoder layer, the counterpart of
+ * bitlinear_ffn_forward:
+ *   q, k, v = BitLinear_q(x), BitLinear_k(x), BitLinear_v(x)    (bf16)
+ *   bitlinear_rope_append(q, k, v), bitlinear_paged_attention
+ *   y = BitLinear_o(attention)                                  ([M][K], bf16)
+ * each exactly as its own call computes it: the three projections as one
+ * grouped launch (pair), then the rotation, the attention, and the o projection.
+ *   x_dev    [in]  [M][K] activations of type xdt, M rows of which the
+ *                  sequences of `seqs` own theirs (rows of no sequence have
+ *                  unspecified outputs)
+ *   q, k, v  [in]  (q_heads, kv_heads, kv_heads) * head_dim x K projections; the
+ *                  three have gains [K] or none has (the RMSNorm ahead of the
+ *                  projection)
+ *   o        [in]  K x (q_heads * head_dim) projection, gain [q_heads *
+ *                  head_dim] or NULL
+ *   q_heads  [in]  q_heads * head_dim is a multiple of 128, at most 65536
+ *   norm_eps [in]  eps of every normalisation given, these and the heads'
+ *   workspace_dev, workspace_bytes [in] bitlinear_workspace_bytes_attn bytes,
+ *                  256-byte aligned
+ * The remaining arguments are those of bitlinear_rope_append and
+ * bitlinear_paged_attention. Argument errors are reported before any launch. */
+int bitlinear_attn_forward(const void *x_dev, bitlinear_dtype xdt, int64_t M,
+                           int64_t K, const bitlinear_projection *q,
+                           const bitlinear_projection *k,
+                           const bitlinear_projection *v,
+                           const bitlinear_projection *o, int64_t q_heads,
+                           const bitlinear_kv_cache *cache,
+                           const bitlinear_seqs *seqs,
+                           const float *inv_freq_dev, int interleaved,
+                           const float *q_head_gain_dev,
+                           const float *k_head_gain_dev, float norm_eps,
+                           float scale, int64_t window, int64_t max_q_len,
+                           void *y_dev, void *workspace_dev,
+                           size_t workspace_bytes, void *cuda_stream);
+
 /* ------------------------------------------------------------- diagnostics */
 
 /* Device-side fault word. Every bounded wait in a kernel gives up after a

@@ -75,7 +75,14 @@ EXPORTS = (
     "bitlinear_rope_append",
     "bitlinear_workspace_bytes_attention",
     "bitlinear_paged_attention",
+    "bitlinear_workspace_bytes_attn",
+    "bitlinear_attn_forward",
 )
+
+
+class _Projection(ctypes.Structure):
+    _fields_ = [("packed_dev", ctypes.c_void_p), ("gamma", ctypes.c_float),
+                ("gain_dev", ctypes.c_void_p)]
 
 
 class _Problem(ctypes.Structure):
@@ -167,6 +174,11 @@ def lib() -> ctypes.CDLL:
         L.bitlinear_paged_attention.restype = ctypes.c_int
         L.bitlinear_paged_attention.argtypes = [p, i64, i64, i64, p, p, f32, i64, i64, p, i64, p,
                                                 p, sz, p]
+        L.bitlinear_workspace_bytes_attn.restype = sz
+        L.bitlinear_workspace_bytes_attn.argtypes = [i64] * 6
+        L.bitlinear_attn_forward.restype = ctypes.c_int
+        L.bitlinear_attn_forward.argtypes = [p, ctypes.c_int, i64, i64, p, p, p, p, i64, p, p, p,
+                                             ctypes.c_int, p, p, f32, f32, i64, i64, p, p, sz, p]
         L.bitlinear_get_fault.restype = ctypes.c_int
         L.bitlinear_get_fault.argtypes = [p, p]
         L.bitlinear_status_string.restype = ctypes.c_char_p
@@ -708,6 +720,55 @@ def _attention_workspace(q, k_cache, page_table, stream):
             q.shape[0], page_table.shape[0], q[:1].numel() // k_cache.shape[3], k_cache.shape[1],
             k_cache.shape[3])
     return _new(q, stream, (0 if need == ctypes.c_size_t(-1).value else need,), torch.uint8)
+
+
+def bitlinear_workspace_bytes_attn(M: int, K: int, seqs: int, q_heads: int, kv_heads: int,
+                                   head_dim: int) -> int:
+    return int(lib().bitlinear_workspace_bytes_attn(M, K, seqs, q_heads, kv_heads, head_dim))
+
+
+def bitlinear_attn_forward(x, q, k, v, o, q_heads: int, k_cache, v_cache, q_start, kv_len,
+                           page_table, inv_freq, gains=(None, None, None, None),
+                           head_gains=(None, None), eps: float = RMSNORM_EPS,
+                           interleaved: bool = False, scale=None, window: int = 0,
+                           max_q_len: int | None = None, y=None, workspace=None, stream=None):
+    """The attention block of a decoder layer for x [M][K]: the q, k and v
+    BitLinears (one grouped launch or pair), ``bitlinear_rope_append``,
+    ``bitlinear_paged_attention`` and the o BitLinear, each as its own call
+    computes it. ``q``, ``k``, ``v`` and ``o`` are (packed, gamma) pairs;
+    ``gains`` gives their RMSNorm gains (q, k and v together), ``head_gains``
+    those of every query and key head; the other arguments are those of the two
+    attention calls. Returns y (bf16 [M][K]; rows of no sequence are
+    unspecified)."""
+    import torch
+    a = _Args()
+    if x.dim() != 2:
+        raise ValueError(f"x must be [M][K], got {tuple(x.shape)}")
+    M, K = x.shape
+    kv_heads, D, S, cache, seqs = _paged(a, k_cache, v_cache, q_start, kv_len, page_table)
+    need = bitlinear_workspace_bytes_attn(M, K, S, q_heads, kv_heads, D)
+    if need == ctypes.c_size_t(-1).value:
+        raise BitLinearError(BITLINEAR_ERR_SHAPE, "bitlinear_workspace_bytes_attn")
+    f32 = torch.float32
+    wide, narrow = q_heads * D, kv_heads * D
+    proj = [_Projection(a.packed(packed, n, k_), float(gamma),
+                        a.ptr(gain, f"gains[{i}]", f32, (k_,)))
+            for i, ((packed, gamma), gain, n, k_) in enumerate(zip(
+                (q, k, v, o), gains, (wide, narrow, narrow, K), (K, K, K, wide)))]
+    if y is None:
+        y = _new(x, stream, (M, K), torch.bfloat16)
+    if workspace is None:
+        workspace = _new(x, stream, (need,), torch.uint8)
+    rc = lib().bitlinear_attn_forward(
+        a.ptr(x, "x"), _xdt(x), M, K, *(ctypes.addressof(p) for p in proj), q_heads, cache, seqs,
+        a.ptr(inv_freq, "inv_freq", f32, (D // 2,)), 1 if interleaved else 0,
+        a.ptr(head_gains[0], "head_gains[0]", f32, (D,)),
+        a.ptr(head_gains[1], "head_gains[1]", f32, (D,)), float(eps),
+        float(D ** -0.5 if scale is None else scale), int(window), int(max_q_len or 0),
+        a.ptr(y, "y", torch.bfloat16, (M, K)), a.ptr(workspace, "workspace", torch.uint8),
+        workspace.numel(), _stream(stream))
+    _check(rc, "bitlinear_attn_forward")
+    return y
 
 
 def bitlinear_get_fault(stream=None) -> tuple[int, int]:

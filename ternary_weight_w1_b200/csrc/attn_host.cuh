@@ -422,3 +422,128 @@ extern "C" int bitlinear_paged_attention(const void *q_dev, int64_t q_stride, in
     return D == 64 ? run_attention<64>(p, *cache, longest * p.work.group, ws, *dev, st)
                    : run_attention<128>(p, *cache, longest * p.work.group, ws, *dev, st);
 }
+
+// ---------------------------------------------------------- attention block
+
+namespace {
+
+// Workspace of bitlinear_attn_forward: the projections' outputs and the
+// attention's (behind q), then the scratch of one step at a time.
+struct AttnBlock {
+    size_t q, k, v, scratch, bytes;      // offsets, and the whole
+    size_t scratch_bytes;
+};
+
+bool attn_block(int64_t M, int64_t K, int64_t seqs, int64_t q_heads, int64_t kv_heads,
+                int64_t head_dim, AttnBlock *b)
+{
+    if (M < 0 || K < 1 || check_paged_shape(M, seqs, q_heads, kv_heads, head_dim) != BITLINEAR_OK)
+        return false;
+    const int64_t wide = q_heads * head_dim, narrow = kv_heads * head_dim;
+    if (K % 128 != 0 || K > kMaxK || wide % 128 != 0 || wide > kMaxK)
+        return false;
+    bitlinear_problem pr[3] = {};
+    for (int i = 0; i < 3; ++i)
+        pr[i] = bitlinear_problem{nullptr, M, K, i == 0 ? wide : narrow, nullptr, 1.0f, nullptr};
+    const size_t project = bitlinear_workspace_bytes_grouped(pr, 3);
+    const size_t attend = bitlinear_workspace_bytes_attention(M, seqs, q_heads, kv_heads, head_dim);
+    const size_t out = bitlinear_workspace_bytes(M, K, wide);
+    if (project == SIZE_MAX || attend == SIZE_MAX || out == SIZE_MAX)
+        return false;
+    const size_t rows = static_cast<size_t>(M) * 2;
+    b->q = 0;
+    b->k = 2 * round_up(rows * wide, 256);
+    b->v = b->k + round_up(rows * narrow, 256);
+    b->scratch = b->v + round_up(rows * narrow, 256);
+    b->scratch_bytes = std::max({project, attend, out});
+    b->bytes = M == 0 ? 0 : b->scratch + b->scratch_bytes;
+    return true;
+}
+
+}  // namespace
+
+extern "C" size_t bitlinear_workspace_bytes_attn(int64_t M, int64_t K, int64_t seqs,
+                                                 int64_t q_heads, int64_t kv_heads,
+                                                 int64_t head_dim)
+{
+    AttnBlock b{};
+    return attn_block(M, K, seqs, q_heads, kv_heads, head_dim, &b) ? b.bytes : SIZE_MAX;
+}
+
+extern "C" int bitlinear_attn_forward(const void *x_dev, bitlinear_dtype xdt, int64_t M, int64_t K,
+                                      const bitlinear_projection *q, const bitlinear_projection *k,
+                                      const bitlinear_projection *v, const bitlinear_projection *o,
+                                      int64_t q_heads, const bitlinear_kv_cache *cache,
+                                      const bitlinear_seqs *seqs, const float *inv_freq_dev,
+                                      int interleaved, const float *q_head_gain_dev,
+                                      const float *k_head_gain_dev, float norm_eps, float scale,
+                                      int64_t window, int64_t max_q_len, void *y_dev,
+                                      void *workspace_dev, size_t workspace_bytes,
+                                      void *cuda_stream)
+{
+    if (q == nullptr || k == nullptr || v == nullptr || o == nullptr)
+        return BITLINEAR_ERR_ARG;
+    bool empty = false;
+    int rc = check_paged(M, q_heads, cache, seqs, &empty);
+    if (rc != BITLINEAR_OK)
+        return rc;
+    if (K < 1)
+        return BITLINEAR_ERR_ARG;
+    if (xdt != BITLINEAR_BF16 && xdt != BITLINEAR_FP32)
+        return BITLINEAR_ERR_DTYPE;
+    const int64_t D = cache->head_dim, wide = q_heads * D, narrow = cache->kv_heads * D;
+    AttnBlock b{};
+    if (!attn_block(M, K, seqs->seqs, q_heads, cache->kv_heads, D, &b))
+        return BITLINEAR_ERR_SHAPE;
+    const bool norm = q->gain_dev != nullptr;
+    if ((k->gain_dev != nullptr) != norm || (v->gain_dev != nullptr) != norm)
+        return BITLINEAR_ERR_ARG;
+    if ((norm || o->gain_dev != nullptr || q_head_gain_dev != nullptr ||
+         k_head_gain_dev != nullptr) &&
+        (!(norm_eps > 0.0f) || !(norm_eps <= FLT_MAX)))
+        return BITLINEAR_ERR_ARG;
+    if (!(scale > 0.0f) || !(scale <= FLT_MAX) || window < 0 || max_q_len < 0 ||
+        (interleaved != 0 && interleaved != 1))
+        return BITLINEAR_ERR_ARG;
+    if (empty)
+        return BITLINEAR_OK;
+    const bitlinear_projection *const projections[4] = {q, k, v, o};
+    for (const bitlinear_projection *p : projections) {
+        if (p->packed_dev == nullptr)
+            return BITLINEAR_ERR_ARG;
+        if (!aligned(p->packed_dev, 16) || !aligned(p->gain_dev, 16))
+            return BITLINEAR_ERR_ALIGN;
+    }
+    if (x_dev == nullptr || y_dev == nullptr || inv_freq_dev == nullptr)
+        return BITLINEAR_ERR_ARG;
+    if (!aligned(x_dev, 16) || !aligned(y_dev, 16) || !aligned(inv_freq_dev, 4) ||
+        !aligned(q_head_gain_dev, 4) || !aligned(k_head_gain_dev, 4))
+        return BITLINEAR_ERR_ALIGN;
+    if (workspace_dev == nullptr || workspace_bytes < b.bytes)
+        return BITLINEAR_ERR_WORKSPACE;
+    if (!aligned(workspace_dev, 256))
+        return BITLINEAR_ERR_ALIGN;
+
+    char *ws = static_cast<char *>(workspace_dev);
+    char *scratch = ws + b.scratch;
+    void *qy = ws + b.q, *ky = ws + b.k, *vy = ws + b.v, *out = ws + b.k / 2;
+    const bitlinear_problem pr[3] = {{x_dev, M, K, wide, q->packed_dev, q->gamma, qy},
+                                     {x_dev, M, K, narrow, k->packed_dev, k->gamma, ky},
+                                     {x_dev, M, K, narrow, v->packed_dev, v->gamma, vy}};
+    const float *const gains[3] = {q->gain_dev, k->gain_dev, v->gain_dev};
+    rc = norm ? bitlinear_forward_grouped_rmsnorm(pr, gains, 3, norm_eps, xdt, scratch,
+                                                  b.scratch_bytes, cuda_stream)
+              : bitlinear_forward_grouped_ws(pr, 3, xdt, scratch, b.scratch_bytes, cuda_stream);
+    if (rc == BITLINEAR_OK)
+        rc = bitlinear_rope_append(qy, wide, ky, narrow, vy, narrow, M, q_heads, cache, seqs,
+                                   inv_freq_dev, interleaved, q_head_gain_dev, k_head_gain_dev,
+                                   norm_eps, qy, wide, cuda_stream);
+    if (rc == BITLINEAR_OK)
+        rc = bitlinear_paged_attention(qy, wide, M, q_heads, cache, seqs, scale, window, max_q_len,
+                                       out, wide, nullptr, scratch, b.scratch_bytes, cuda_stream);
+    if (rc != BITLINEAR_OK)
+        return rc;
+    return forward_impl(out, BITLINEAR_BF16, M, wide, o->packed_dev, o->gamma, K, y_dev, scratch,
+                        b.scratch_bytes, cuda_stream, nullptr, nullptr, nullptr,
+                        BITLINEAR_PATH_AUTO, 0, o->gain_dev, norm_eps);
+}

@@ -176,3 +176,68 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
         with pytest.raises(bl.BitLinearError) as e:
             call(dict(host_step(), k_cache=torch.zeros(4, 2, 16, 80, dtype=torch.bfloat16)))
         assert e.value.status == bl.BITLINEAR_ERR_SHAPE
+
+
+class Projection(ctypes.Structure):
+    _fields_ = [("packed_dev", ctypes.c_void_p), ("gamma", ctypes.c_float),
+                ("gain_dev", ctypes.c_void_p)]
+
+
+def block(**kw):
+    cache, seqs = descriptors(kw)
+    gains = kw.pop("gains", (None,) * 4)
+    proj = [Projection(kw.pop("packed", FAKE) if i == 3 else FAKE, 1.0, g)
+            for i, g in enumerate(gains)]
+    a = dict(x=FAKE, xdt=0, M=3, K=256, q=ctypes.addressof(proj[0]), kk=ctypes.addressof(proj[1]),
+             vv=ctypes.addressof(proj[2]), o=ctypes.addressof(proj[3]), heads=4,
+             cache=ctypes.addressof(cache), sq=ctypes.addressof(seqs), f=FAKE, inter=0, qg=None,
+             kg=None, eps=1e-6, scale=0.125, window=0, max_q=0, y=FAKE, ws=FAKE, wsb=BIG,
+             stream=None)
+    a.update(kw)
+    return bl.lib().bitlinear_attn_forward(*a.values())
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=None), bl.BITLINEAR_ERR_ARG),
+    (dict(o=None), bl.BITLINEAR_ERR_ARG),
+    (dict(packed=None), bl.BITLINEAR_ERR_ARG),
+    (dict(x=None), bl.BITLINEAR_ERR_ARG),
+    (dict(y=None), bl.BITLINEAR_ERR_ARG),
+    (dict(f=None), bl.BITLINEAR_ERR_ARG),
+    (dict(k=None), bl.BITLINEAR_ERR_ARG),
+    (dict(M=-1), bl.BITLINEAR_ERR_ARG),
+    (dict(K=0), bl.BITLINEAR_ERR_ARG),
+    (dict(xdt=5), bl.BITLINEAR_ERR_DTYPE),
+    (dict(K=200), bl.BITLINEAR_ERR_SHAPE),
+    (dict(K=65536 + 128), bl.BITLINEAR_ERR_SHAPE),
+    (dict(heads=3, kv_heads=3), bl.BITLINEAR_ERR_SHAPE),      # 192 wide: no multiple of 128
+    (dict(heads=2048), bl.BITLINEAR_ERR_SHAPE),               # 131072 wide
+    (dict(gains=(FAKE, None, FAKE, None)), bl.BITLINEAR_ERR_ARG),
+    (dict(gains=(None, None, None, FAKE), eps=0.0), bl.BITLINEAR_ERR_ARG),
+    (dict(kg=FAKE, eps=-1.0), bl.BITLINEAR_ERR_ARG),
+    (dict(gains=(FAKE, FAKE, FAKE + 4, None)), bl.BITLINEAR_ERR_ALIGN),
+    (dict(scale=0.0), bl.BITLINEAR_ERR_ARG),
+    (dict(window=-1), bl.BITLINEAR_ERR_ARG),
+    (dict(max_q=-1), bl.BITLINEAR_ERR_ARG),
+    (dict(inter=3), bl.BITLINEAR_ERR_ARG),
+    (dict(x=FAKE + 2), bl.BITLINEAR_ERR_ALIGN),
+    (dict(y=FAKE + 8), bl.BITLINEAR_ERR_ALIGN),
+    (dict(ws=None), bl.BITLINEAR_ERR_WORKSPACE),
+    (dict(wsb=1000), bl.BITLINEAR_ERR_WORKSPACE),
+    (dict(ws=FAKE + 16), bl.BITLINEAR_ERR_ALIGN),
+    (dict(M=0), bl.BITLINEAR_OK),
+    (dict(seqs=0), bl.BITLINEAR_OK),
+])
+def test_block_refusals(kw, status):
+    assert block(**dict(kw)) == status
+
+
+def test_block_workspace_bytes():
+    size_max = ctypes.c_size_t(-1).value
+    ws = bl.bitlinear_workspace_bytes_attn
+    assert ws(0, 2560, 1, 20, 5, 128) == 0
+    assert ws(1, 2560, 1, 20, 5, 128) >= bl.bitlinear_workspace_bytes_attention(1, 1, 20, 5, 128)
+    assert ws(100, 2560, 1, 20, 5, 128) > 100 * (2 * 2560 + 2 * 640) * 2
+    for bad in ((1, 2500, 1, 20, 5, 128), (1, 2560, 1, 3, 3, 64), (1, 2560, 1, 20, 5, 32),
+                (-1, 2560, 1, 20, 5, 128)):
+        assert ws(*bad) == size_max
