@@ -93,14 +93,12 @@ struct Cfg {
     static constexpr int TILE_BYTES = BN * D * 2;              // keys or values of a tile
     static constexpr int STAGES = D == 128 ? 4 : 8;
     static constexpr int OUT_BYTES = 32 * 64;                  // staged output of one warp
-    static constexpr int MAX_BYTES = 2 * 2 * HALF * 4;         // exchanged maxima
     static constexpr int BARRIERS = 2 * STAGES + 18;
-    // shared memory, all of it dynamic: queries, ring, staged output, maxima,
+    // shared memory, all of it dynamic: queries, ring, the warps' staging,
     // barriers, TMEM address and abort flag
     static constexpr int RING_AT = 2 * Q_BYTES;
     static constexpr int OUT_AT = RING_AT + STAGES * TILE_BYTES;
-    static constexpr int MAX_AT = OUT_AT + SOFTMAX_WARPS * OUT_BYTES;
-    static constexpr int BAR_AT = MAX_AT + MAX_BYTES;
+    static constexpr int BAR_AT = OUT_AT + SOFTMAX_WARPS * OUT_BYTES;
     static constexpr int SMEM_BYTES = BAR_AT + BARRIERS * 8 + 16;
 };
 
@@ -516,11 +514,12 @@ __global__ void __launch_bounds__(THREADS, 1)
         const uint32_t o_addr = o_tmem(h) + lane_off + part * (D / 2);
         char *out = smem + C::OUT_AT + warp * C::OUT_BYTES;
         const int pair_bar = 1 + h * 4 + (warp & 3);           // the two warps of 32 rows
-        // the two threads' maxima of a row, [step parity][half][row][part] in bf16
-        uint16_t *const my_max =
-            reinterpret_cast<uint16_t *>(smem + C::MAX_AT) + (h * HALF + in_half) * 2 + part;
-        const uint32_t *const both_max =
-            reinterpret_cast<const uint32_t *>(smem + C::MAX_AT) + h * HALF + in_half;
+        const char *other = smem + C::OUT_AT + (warp ^ 4) * C::OUT_BYTES;
+        // A row's other thread finds its maximum (of two steps in turn) and sum in
+        // this warp's staging rows, which hold output only between the items'
+        // last barrier and the next one's first maximum.
+        float *const my_max = reinterpret_cast<float *>(out) + lane;
+        const float *const other_max = reinterpret_cast<const float *>(other) + lane;
         uint32_t ph = 0;                                       // parity of the tile's barriers
         bool ok = true;
         while (ok && left > 0) {
@@ -581,19 +580,15 @@ __global__ void __launch_bounds__(THREADS, 1)
                         for (int k = 0; k < 4; ++k)
                             t4[k] = max3(__uint_as_float(s[i + 2 * k]),
                                          __uint_as_float(s[i + 2 * k + 1]), t4[k]);
-                    // The row's maximum from both its threads, rounded to bf16 (m
-                    // need not be the maximum itself, only the same in both and
-                    // near it). The barrier also takes the two warps' verdict on
-                    // their waits, so that neither is left alone at the next one.
-                    my_max[b * 4 * HALF] = __bfloat16_as_ushort(
-                        __float2bfloat16_rn(fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]))));
+                    // The row's maximum from both its threads. The barrier also
+                    // takes the two warps' verdict on their waits, so that neither
+                    // is left alone at the next one.
+                    const float mine = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                    my_max[b * 32] = mine;
                     ok = named_bar_and(pair_bar, 64, ok);
                     if (!ok)
                         break;
-                    const uint32_t mx = both_max[b * 2 * HALF];
-                    const float top = fmaxf(__uint_as_float(mx << 16),
-                                            __uint_as_float(mx & 0xffff0000u)) *
-                                      p.scale_log2;
+                    const float top = fmaxf(mine, other_max[b * 32]) * p.scale_log2;
                     const bool raise = top > m + RESCALE_AT;           // also from -inf
                     if (__any_sync(0xffffffffu, raise)) {
                         const float f = raise ? exp2_approx(m - top) : 1.0f;
@@ -661,11 +656,11 @@ __global__ void __launch_bounds__(THREADS, 1)
                 // the last products; the row's sum from both its threads
                 ok = ok && wait(o_done(h, 1), ph ^ 1u);
                 if (!idle) {
-                    reinterpret_cast<float *>(out)[lane] = l;
+                    // (the last products are done, so the other thread has read the
+                    // maxima)
+                    my_max[64] = l;
                     ok = named_bar_and(pair_bar, 64, ok);
-                    const float *other = reinterpret_cast<const float *>(
-                        smem + C::OUT_AT + (warp ^ 4) * C::OUT_BYTES);
-                    l = part == 0 ? l + other[lane] : other[lane] + l;
+                    l = part == 0 ? l + other_max[64] : other_max[64] + l;
                     ok = named_bar_and(pair_bar, 64, ok);      // both sums are read
                 }
                 if (!ok)
