@@ -584,7 +584,7 @@ size_t bitlinear_workspace_bytes_attention(int64_t tokens, int64_t seqs,
  * and whole prompts are the same call and may be mixed.
  *   q_dev, q_stride, tokens, q_heads, cache, seqs [in] as for
  *                  bitlinear_rope_append; q_heads a multiple of kv_heads
- *   scale    [in]  finite and > 0
+ *   scale    [in]  > 0 and below 2^127
  *   window   [in]  keys that a token sees, itself included; 0: all before it
  *   max_q_len [in] the largest number of rows of any sequence when the host
  *                  knows it, or 0. A hint that chooses the kernels: a smaller

@@ -381,7 +381,7 @@ extern "C" int bitlinear_paged_attention(const void *q_dev, int64_t q_stride, in
     int rc = check_paged(tokens, q_heads, cache, seqs, &empty);
     if (rc != BITLINEAR_OK)
         return rc;
-    if (!(scale > 0.0f) || !(scale <= FLT_MAX) || window < 0 || max_q_len < 0)
+    if (!(scale > 0.0f) || !(scale <= FLT_MAX / 2) || window < 0 || max_q_len < 0)
         return BITLINEAR_ERR_ARG;
     if (empty)
         return BITLINEAR_OK;
@@ -502,7 +502,7 @@ extern "C" int bitlinear_attn_forward(const void *x_dev, bitlinear_dtype xdt, in
          k_head_gain_dev != nullptr) &&
         (!(norm_eps > 0.0f) || !(norm_eps <= FLT_MAX)))
         return BITLINEAR_ERR_ARG;
-    if (!(scale > 0.0f) || !(scale <= FLT_MAX) || window < 0 || max_q_len < 0 ||
+    if (!(scale > 0.0f) || !(scale <= FLT_MAX / 2) || window < 0 || max_q_len < 0 ||
         (interleaved != 0 && interleaved != 1))
         return BITLINEAR_ERR_ARG;
     if (empty)

@@ -131,6 +131,7 @@ def test_append_refusals(kw, status):
     (dict(scale=-1.0), bl.BITLINEAR_ERR_ARG),
     (dict(scale=float("nan")), bl.BITLINEAR_ERR_ARG),
     (dict(scale=float("inf")), bl.BITLINEAR_ERR_ARG),
+    (dict(scale=3e38), bl.BITLINEAR_ERR_ARG),             # its product with log2 e overflows
     (dict(window=-1), bl.BITLINEAR_ERR_ARG),
     (dict(max_q=-1), bl.BITLINEAR_ERR_ARG),
     (dict(ys=128), bl.BITLINEAR_ERR_SHAPE),

@@ -151,6 +151,17 @@ def test_many_sequences():
     check(Step(lens, (4, 1, 64), 16, seed=12), max_q_len=1)
 
 
+def test_five_thousand_sequences():
+    lens = [(1, 1 + i % 5) for i in range(5000)] + [(40, 60)]
+    check(Step(lens, (2, 1, 64), 16, seed=24))
+
+
+@pytest.mark.parametrize("heads", [(130, 1, 64), (200, 2, 64), (128, 1, 128)])
+def test_many_heads_per_key_head(heads):
+    # a token of more rows than half an item of the chunk kernel is cut anywhere
+    check(Step([(1, 70), (3, 40), (20, 33)], heads, 16, seed=25))
+
+
 def test_one_long_sequence_among_short_ones():
     check(Step([(1, 5), (1, 40000), (1, 3), (1, 64)], (8, 2, 128), 128, seed=13), max_q_len=1)
 
@@ -172,6 +183,39 @@ def test_strided_queries_and_outputs():
     step.check_attention(y)
     assert (out[:, :128] == CANARY).all() and (out[:, 384:] == CANARY).all()
     assert torch.equal(step.attend(q=wide[:, 64:320].view(step.rows, 4, 64)).flatten(1), y)
+
+
+@pytest.mark.parametrize("offset", [8, 24])
+def test_rows_aligned_to_sixteen_bytes_only(offset):
+    step = Step([(1, 77), (90, 100)], (4, 2, 64), 16, seed=26)
+    wide = torch.full((step.rows, 256 + 40), math.nan, dtype=torch.bfloat16, device="cuda")
+    wide[:, offset:offset + 256] = step.q.flatten(1)
+    out = torch.full((step.rows, 256 + 40), CANARY, dtype=torch.bfloat16, device="cuda")
+    step.check_attention(step.attend(q=wide[:, offset:offset + 256],
+                                     y=out[:, offset:offset + 256]))
+    assert (out[:, :offset] == CANARY).all() and (out[:, offset + 256:] == CANARY).all()
+
+
+@pytest.mark.parametrize("q", [1, 150])
+def test_a_cache_of_more_than_two_to_the_32_elements(q):
+    step = Step([(q, 300), (1, 90)], (8, 2, 128), 64, seed=27)
+    pages = step.k_cache.shape[0]
+    first = 2 ** 32 // (2 * 64 * 128)                  # its elements are past 32 bits
+    caches = []
+    for c in (step.k_cache, step.v_cache):
+        big = torch.empty((first + pages, 2, 64, 128), dtype=torch.bfloat16, device="cuda")
+        big[first:] = c
+        caches.append(big)
+    table = torch.where(step.table >= 0, step.table + first, step.table)
+    y = bl.bitlinear_paged_attention(step.q, *caches, step.q_start, step.kv_len, table)
+    step.check_attention(y)
+    # and the append reaches the same places
+    f = torch.zeros(64, device="cuda")                 # no rotation: the keys as they are
+    bl.bitlinear_rope_append(step.q, step.k, step.v, *caches, step.q_start, step.kv_len, table, f)
+    page = table[0].long()[torch.arange(300 - q, 300, device="cuda") // 64]
+    slot = torch.arange(300 - q, 300, device="cuda") % 64
+    assert torch.equal(caches[0][page, :, slot], step.k[:q])
+    assert torch.equal(caches[1][page, :, slot], step.v[:q])
 
 
 def test_a_hint_that_is_too_small_only_costs_time():
@@ -229,6 +273,35 @@ def test_two_graphs_share_a_workspace_one_after_the_other():
         outs[i].zero_()
         graphs[i].replay()
         (a, b)[i].check_attention(outs[i])
+
+
+def test_replays_in_a_row_on_one_workspace():
+    # flags and parts of one replay are never taken for another's
+    steps = [Step([(300, 900), (1, 2000)], (8, 2, 64), 16, seed=28),
+             Step([(700, 700)], (4, 1, 128), 64, seed=29)]
+    need = max(bl.bitlinear_workspace_bytes_attention(s.rows, len(s.lens), s.hq, s.hkv, s.d)
+               for s in steps)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    outs, graphs = [], []
+    for s in steps:
+        y = torch.zeros((s.rows, s.hq, s.d), dtype=torch.bfloat16, device="cuda")
+        s.attend(y=y, workspace=ws)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            s.attend(y=y, workspace=ws)
+        outs.append(y)
+        graphs.append(g)
+    first = [o.clone() for o in outs]
+    for i, s in enumerate(steps):
+        s.check_attention(first[i])
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for n in range(150):
+        i = (n * 7 // 3) % 2
+        outs[i].fill_(CANARY)
+        graphs[i].replay()
+        wrong += (outs[i].view(torch.int16) != first[i].view(torch.int16)).sum()
+    assert wrong.item() == 0
 
 
 def test_streams():
