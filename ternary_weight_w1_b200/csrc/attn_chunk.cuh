@@ -10,15 +10,21 @@
 //   O_h += P_h V           P_h from TMEM, V from shared memory as it lies there
 //                          (its channels contiguous: an MN-major operand)
 // Each half has two S buffers, which the two steps of a 128-key tile take in
-// turn: the products of one step run while the warps compute the exponentials
-// of the other, so neither waits for the other's latency. (With one buffer of
-// 128 keys, and the halves alone overlapping, a tile took 4580 clocks at D =
-// 128, of which the tensor pipe worked 45%.)
+// turn: the products of one step run while the warps compute the exponentials of
+// the other. A row's 64 scores of a step belong to two threads of two warps,
+// which exchange their maxima through shared memory.
 //
-// A row's 64 scores of a step belong to two threads of two warps, which exchange
-// their maxima through shared memory. (With one thread a row, eight warps, a
-// step's chain of loads, maxima, exponentials and stores took 1850 clocks: two
-// warps a scheduler do not hide their latencies.)
+// What bounds it at D = 128: a tile of both halves takes 3700 to 3900 clocks (2.2
+// us), against 2048 of the tensor pipe at its full rate. Products of N = 64 cost
+// the pipe nearly what those of N = 128 do, so the scores take 2048 of these
+// clocks instead of 1024, and the warps' chain of load, maximum, exponentials and
+// store the rest. Measured beside it: one S buffer of 128 keys a half with one
+// issuing warp 4580 clocks, with two issuing warps and two threads a row 4400;
+// eight softmax warps with a row a thread 4000 (the same time where the clock is
+// held down by power, but 20% slower on windowed prompts of 64 channels); every
+// pair of exponentials on the special-function unit 4% slower, every second on
+// the multiply-add pipe 4% slower. 4096 rows behind 28672 keys, 64 heads on 8:
+// 3.7 to 4.5 ms, 920 to 1110 TFLOP/s by the clock that power leaves.
 //
 // Items that are split into up to four parts, as most split ones are, are joined
 // here: a worker computes the part of the item that began before its run first
@@ -52,6 +58,7 @@ constexpr int SOFTMAX_WARPS = 16;
 constexpr int THREADS = (SOFTMAX_WARPS + 4) * 32;
 constexpr int TMEM_COLS = 512;
 constexpr int JOIN = 3;                // parts behind its own that a worker joins
+
 __device__ __forceinline__ uint64_t ld_acquire_u64(const uint64_t *p)
 {
     uint64_t v;
@@ -531,7 +538,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             const bool whole = from_start && to_end;
             const bool active = h < halves_of();
             if (!whole)
-                head[from_start ? 1 : 0] = paged::PartHeader{rows, to_end ? 0 : 1, cur.v.q0, cur.h + w.kv_heads * cur.m};
+                head[from_start ? 1 : 0] =
+                    paged::PartHeader{rows, to_end ? 0 : 1, cur.v.q0, cur.h + w.kv_heads * cur.m};
             // this thread's row of the item, and those of its half
             const int r = h * half_rows + in_half;
             const int end = min(rows, (h + 1) * half_rows);
@@ -684,7 +692,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             break;
                         if (lane == 0)
                             flag = wait_flag(p.parts.flags + (worker + 1 + k) * 16 + warp, p.nonce,
-                                             abort_flag, p.wait_limit_ns);
+                                         abort_flag, p.wait_limit_ns);
                         flag = __shfl_sync(0xffffffffu, flag, 0);
                         ok = named_bar_and(pair_bar, 64, flag != 0);
                         if (!ok)
@@ -730,9 +738,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int at = r - lane + i * 8 + (lane >> 2);
-                        dst[i] = at < end ? reinterpret_cast<char *>(
-                                                p.y + row_of(cur, at, p.y_stride) + part * (D / 2)) +
-                                                (lane & 3) * 16
+                        uint16_t *row = p.y + row_of(cur, at, p.y_stride) + part * (D / 2);
+                        dst[i] = at < end ? reinterpret_cast<char *>(row) + (lane & 3) * 16
                                           : nullptr;
                     }
                     uint4 *const mine = reinterpret_cast<uint4 *>(out + lane * 64);
@@ -791,9 +798,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                         p.lse[(cur.v.q0 + tok) * static_cast<int64_t>(p.q_heads) +
                               cur.h * w.group + rr - tok * w.group] = lse_of(m, l);
                 } else {
-                    float4 *mine = reinterpret_cast<float4 *>(
-                                       p.parts.o + static_cast<int64_t>(slot) * p.parts.row_cap * D) +
-                                   static_cast<int64_t>(part * (D / 8)) * p.parts.row_cap + r;
+                    float4 *mine = const_cast<float4 *>(o_parts) + slot * slot_o;
 #pragma unroll 1
                     for (int c = 0; c < D / 64; ++c) {
                         uint32_t o[32];
@@ -927,8 +932,8 @@ __global__ void __launch_bounds__(MERGE_THREADS) join_kernel(const MergeParams p
                 for (int k = 0; k < 8; ++k)
                     if (k0 + k < parts) {
                         ml[k] = p.parts.ml[slot(k0 + k) + r];
-                        v[k] = reinterpret_cast<const float4 *>(
-                            p.parts.o)[slot(k0 + k) * (D / 4) + static_cast<int64_t>(c4) * row_cap + r];
+                        v[k] = reinterpret_cast<const float4 *>(p.parts.o)[
+                            slot(k0 + k) * (D / 4) + static_cast<int64_t>(c4) * row_cap + r];
                     }
 #pragma unroll
                 for (int k = 0; k < 8; ++k)

@@ -5,7 +5,7 @@
 
 namespace {
 
-constexpr int kAttnMaxGrid = 192;                    // blocks of a launch; the parts are sized by it
+constexpr int kAttnMaxGrid = 192;                    // SMs that a launch uses at most
 constexpr int64_t kAttnMaxSeqs = 32 * paged::MAX_GROUPS;
 constexpr int64_t kAttnMaxKeys = int64_t(1) << 30;   // page slots of a sequence
 constexpr int64_t kAttnMaxRows = int64_t(1) << 30;   // tokens * query heads
@@ -94,10 +94,9 @@ paged::Seqs device_seqs(const bitlinear_kv_cache &c, const bitlinear_seqs &s, in
 template <int D>
 cudaError_t launch_rope(const rope::Params &p, bool interleaved, int grid, cudaStream_t st)
 {
-    return interleaved
-               ? launch(rope::rope_append_kernel<D, true>, dim3(grid), dim3(rope::THREADS), 0, st, p)
-               : launch(rope::rope_append_kernel<D, false>, dim3(grid), dim3(rope::THREADS), 0, st,
-                        p);
+    return launch(interleaved ? rope::rope_append_kernel<D, true>
+                              : rope::rope_append_kernel<D, false>,
+                  dim3(grid), dim3(rope::THREADS), 0, st, p);
 }
 
 // ---------------------------------------------------------------- attention
@@ -151,7 +150,8 @@ size_t parts_layout(int64_t workers, int64_t row_cap, int64_t head_dim, bool fla
     const size_t hb = round_up(static_cast<size_t>(2 * workers) * sizeof(paged::PartHeader), 256);
     const size_t mb = round_up(static_cast<size_t>(2 * workers * row_cap) * sizeof(float2), 256);
     const size_t ob = round_up(static_cast<size_t>(2 * workers * row_cap * head_dim) * 4, 256);
-    const size_t fb = flags ? round_up(static_cast<size_t>(16 * workers) * sizeof(uint64_t), 256) : 0;
+    const size_t fb =
+        flags ? round_up(static_cast<size_t>(16 * workers) * sizeof(uint64_t), 256) : 0;
     if (out != nullptr) {
         out->headers = reinterpret_cast<paged::PartHeader *>(base);
         out->ml = reinterpret_cast<float2 *>(base + hb);
@@ -178,8 +178,8 @@ AttnLayout attn_layout(int64_t rows, int64_t head_dim, char *base)
     l.bytes = parts_layout(kAttnMaxGrid * blocks * attn::rows::WARPS,
                            std::min<int64_t>(rows, kRowsKernelMax), head_dim, false, base, &l.rows);
     if (rows > kRowsKernelMax)
-        l.bytes += parts_layout(kAttnMaxGrid, std::min<int64_t>(rows, 2 * attn::chunk::HALF), head_dim,
-                                true, base + l.bytes, &l.chunk);
+        l.bytes += parts_layout(kAttnMaxGrid, std::min<int64_t>(rows, 2 * attn::chunk::HALF),
+                                head_dim, true, base + l.bytes, &l.chunk);
     return l;
 }
 

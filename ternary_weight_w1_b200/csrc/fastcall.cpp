@@ -9,6 +9,8 @@
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <cmath>
+
 #include "../../include/bitlinear.h"
 
 namespace {
@@ -209,13 +211,13 @@ PyObject *bind(PyObject *, PyObject *const *a, Py_ssize_t n)
     Py_RETURN_NONE;
 }
 
+template <typename F>
+PyCFunction method(F *f) { return reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)); }
+
 PyMethodDef g_methods[] = {
-    {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind)), METH_FASTCALL, nullptr},
-    {"rope_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope_append)),
-     METH_FASTCALL, nullptr},
-    {"paged_attention",
-     reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(paged_attention)), METH_FASTCALL,
-     nullptr},
+    {"bind", method(bind), METH_FASTCALL, nullptr},
+    {"rope_append", method(rope_append), METH_FASTCALL, nullptr},
+    {"paged_attention", method(paged_attention), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_fastcall", nullptr, -1, g_methods,

@@ -276,8 +276,8 @@ __device__ __forceinline__ int64_t quotient(int64_t n, int64_t d)
 
 // Deals the launch's units: those that worker `worker` has from the first tile
 // that begins in its run, where `cur` is set (none: 0). A run is never shorter
-// than a tile, so that an item's parts lie in successive workers. Every warp of the block calls it (`workers` workers in
-// all); `sums` is shared memory for MAX_GROUPS numbers that must not be used
+// than a tile, so that an item's parts lie in successive workers. Every warp of
+// the block calls it (`workers` workers in all); `sums` is shared memory for MAX_GROUPS numbers that must not be used
 // for anything else until the block has met again. Up to 32 sequences every
 // warp counts by itself, without a barrier.
 template <int BN>

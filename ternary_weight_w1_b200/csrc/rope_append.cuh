@@ -11,8 +11,8 @@
 // its warps find the rows' sequences and compute the rows' cosines and sines
 // once into shared memory (the head count is what shares them). A thread keeps
 // 16 channels, 8 c .. and D / 2 + 8 c .., which are eight whole pairs in either
-// order, and takes them of every head of its share, so a row's cosines and sines are read from shared memory once
-// per thread, a pair never leaves a thread, and a head's sum of squares is a
+// order, and takes them of every head of its share, so a row's cosines and sines
+// are read from shared memory once per thread, a pair never leaves a thread, and a head's sum of squares is a
 // shuffle over D / 16 threads. Its next heads are on their way to shared memory
 // meanwhile, each thread's to its own place, so no barrier is needed. The angle p f is taken
 // in double and reduced by whole turns there: at position 10^5 an fp32 product
@@ -120,8 +120,8 @@ __global__ void __launch_bounds__(THREADS) rope_append_kernel(const Params p)
     __shared__ __align__(16) float sines[MAX_ROWS][INTERLEAVED ? D : HALF];
     __shared__ __align__(16) float gains[2][D];         // of the queries, of the keys
     __shared__ uint4 staged[STAGES][2][THREADS];        // a thread's own next units
-    __shared__ int64_t slot[MAX_ROWS];      // the row's element offset in the caches (head 0), -1: none
-    __shared__ int posn[MAX_ROWS];          // the row's position, -1: no row of a sequence
+    __shared__ int64_t slot[MAX_ROWS];      // a row's first element in the caches, -1: none
+    __shared__ int posn[MAX_ROWS];          // a row's position, -1: no row of a sequence
 
     pdl_wait();
     pdl_launch_dependents();
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(THREADS) rope_append_kernel(const Params p)
         if (posn[r] < 0)
             continue;
         constexpr double TURN = 6.283185307179586476925;
-        const double angle = static_cast<double>(posn[r]) * static_cast<double>(__ldg(p.inv_freq + f));
+        const double angle = posn[r] * static_cast<double>(__ldg(p.inv_freq + f));
         const float a = static_cast<float>(angle - rint(angle * (1.0 / TURN)) * TURN);
         const float co = cosf(a), si = sinf(a);
         if (INTERLEAVED) {
