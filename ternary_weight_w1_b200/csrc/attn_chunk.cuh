@@ -316,11 +316,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     // behind them.
     auto s_tmem = [&](int h, int b) { return tmem + h * 128 + b * STEP; };
     auto o_tmem = [&](int h) { return tmem + 256 + h * 128; };
-    // tiles of the item that begin in the `left` units of this run
-    auto parts_tiles = [&](int64_t left) {
-        const int64_t n = cur.t.end - cur.tile, in_run = (left + cur.units - 1) / cur.units;
-        return static_cast<int>(n < in_run ? n : in_run);
-    };
     const int half_rows = w.item_rows / 2;                     // whole tokens, at most HALF rows
     auto rows_of = [&]() { return min(w.item_rows, cur.v.qlen * w.group - cur.m * w.item_rows); };
     auto halves_of = [&]() { return rows_of() > half_rows ? 2 : 1; };
@@ -342,7 +337,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t ph = 0, armed = 0;                            // armed: stages in flight, as bits
         bool ok = true;
         while (ok && left > 0) {
-            const int nt = parts_tiles(left);
+            const int nt = cur.run_tiles(w, left);
             for (int j = 0; ok && j < nt; ++j) {
                 const int sub = lane % subs, ch = (lane / subs) % C::CH;
                 const int key = (cur.tile + j) * BN + sub * box;
@@ -372,7 +367,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
             }
-            left -= static_cast<int64_t>(nt) * cur.units;
+            left -= cur.run_units(w, nt);
             if (ok && left > 0)
                 cur.next_item(w);
         }
@@ -411,7 +406,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             umma_commit(s_full(h, b));
         };
         while (ok && left > 0) {
-            const int nt = parts_tiles(left);
+            const int nt = cur.run_tiles(w, left);
             if (h < halves_of()) {
                 int k_stage = st;
                 ok = wait(q_ready(h), q_ph) && wait(full(st), ph);
@@ -501,7 +496,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     next_stage();
                 }
             }
-            left -= static_cast<int64_t>(nt) * cur.units;
+            left -= cur.run_units(w, nt);
             if (ok && left > 0)
                 cur.next_item(w);
         }
@@ -530,7 +525,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         uint32_t ph = 0;                                       // parity of the tile's barriers
         bool ok = true;
         while (ok && left > 0) {
-            const int nt = parts_tiles(left);
+            const int nt = cur.run_tiles(w, left);
             const bool from_start = cur.tile == cur.t.begin;
             const bool to_end = cur.tile + nt == cur.t.end;
             const int rows = rows_of();
@@ -827,7 +822,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                 }
             }
-            left -= static_cast<int64_t>(nt) * cur.units;
+            left -= cur.run_units(w, nt);
             if (left > 0)
                 cur.next_item(w);
         }
@@ -842,7 +837,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         int fetched[2] = {0, 0};
         bool ok = true;
         while (ok && left > 0) {
-            const int nt = parts_tiles(left);
+            const int nt = cur.run_tiles(w, left);
             const int tok = cur.v.q0 + w.by_group(cur.m * w.item_rows);
             for (int h = 0; ok && h < halves_of(); ++h) {
                 ok = wait(q_free(h), ph[h] ^ 1u);
@@ -859,7 +854,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 __syncwarp();
             }
-            left -= static_cast<int64_t>(nt) * cur.units;
+            left -= cur.run_units(w, nt);
             if (left > 0)
                 cur.next_item(w);
         }

@@ -62,7 +62,7 @@ __device__ __forceinline__ int page_of(const Seqs &q, int s, int c)
 // sequence and key head, where row r is query head r % group of token r / group, so the
 // query heads that share a key head share its tiles. An item takes `full` units
 // per tile of BN keys that any of its rows sees, or `half` when it has no more
-// than half its rows. All units of a launch, items in order and key heads
+// than half its rows, and `start` units ahead of its first tile's. All units of a launch, items in order and key heads
 // outermost, are dealt to the workers in equal contiguous runs; a tile belongs to
 // the run that it begins in: a long sequence is split wherever a run ends, and a batch
 // of ragged ones stays balanced without the host knowing a length. A worker
@@ -89,6 +89,7 @@ struct Work {
     int kv_heads;
     int item_rows;         // rows of an item
     int full, half;        // units of a tile
+    int start;             // and of an item besides those of its tiles
     int window;            // 0: none
     int min_rows, max_rows;  // sequences of this launch: min_rows <= qlen * group <= max_rows
 };
@@ -177,7 +178,7 @@ __device__ __forceinline__ int64_t seq_units(const Work &w, int g)
     int64_t n = 0;
     if (v.qlen > 0 && !many) {
         const Tiles t = item_tiles<BN>(w, v, 0);
-        n = (t.end - t.begin) * tile_units(w, v, 0);
+        n = (t.end - t.begin) * tile_units(w, v, 0) + w.start;
     }
     for (unsigned left = __ballot_sync(0xffffffffu, many); left != 0; left &= left - 1) {
         const int at = __ffs(left) - 1;
@@ -188,7 +189,7 @@ __device__ __forceinline__ int64_t seq_units(const Work &w, int g)
         int64_t sum = 0;
         for (int m = lane; m * w.item_rows < x.qlen * w.group; m += 32) {
             const Tiles t = item_tiles<BN>(w, x, m);
-            sum += (t.end - t.begin) * tile_units(w, x, m);
+            sum += (t.end - t.begin) * tile_units(w, x, m) + w.start;
         }
         sum = warp_sum(sum);
         if (lane == at)
@@ -249,7 +250,7 @@ struct Cursor {
             int64_t c = 0;
             if (k0 + lane < items) {
                 const Tiles x = item_tiles<BN>(w, v, item_at(k0 + lane, items));
-                c = (x.end - x.begin) * tile_units(w, v, item_at(k0 + lane, items));
+                c = (x.end - x.begin) * tile_units(w, v, item_at(k0 + lane, items)) + w.start;
             }
             const int64_t sum = warp_scan(c);
             const unsigned in = __ballot_sync(0xffffffffu, off < sum);
@@ -262,9 +263,29 @@ struct Cursor {
             off -= __shfl_sync(0xffffffffu, sum, 31);
         }
         open(w);
-        const int tiles = static_cast<int>((off + units - 1) / units);
+        if (off == 0)
+            return 0;
+        const int tiles = begin_in(off, w.start);
         tile = t.begin + tiles;
-        return static_cast<int>(static_cast<int64_t>(tiles) * units - off);
+        return static_cast<int>(w.start + static_cast<int64_t>(tiles) * units - off);
+    }
+
+    // Tiles that begin in n units from here, the first `ahead` of which begin none
+    // but the one that stands here.
+    __device__ __forceinline__ int begin_in(int64_t n, int ahead) const
+    {
+        return static_cast<int>(max((n - ahead + units - 1) / units, static_cast<int64_t>(1)));
+    }
+
+    // Tiles of the item that begin in the `left` (> 0) units of the run, and the
+    // units that n of them take.
+    __device__ __forceinline__ int run_tiles(const Work &w, int64_t left) const
+    {
+        return min(begin_in(left, tile == t.begin ? w.start : 0), t.end - tile);
+    }
+    __device__ __forceinline__ int64_t run_units(const Work &w, int n) const
+    {
+        return static_cast<int64_t>(n) * units + (tile == t.begin ? w.start : 0);
     }
 };
 
@@ -302,8 +323,9 @@ __device__ __forceinline__ int64_t deal(const Work &w, int worker, int workers, 
         per_head = warp_sum(per_head);
     }
     const int64_t units = per_head * w.kv_heads;
-    if (workers > units / w.full)
-        workers = static_cast<int>(max(units / w.full, static_cast<int64_t>(1)));
+    const int shortest = w.full + w.start;
+    if (workers > units / shortest)
+        workers = static_cast<int>(max(units / shortest, static_cast<int64_t>(1)));
     if (worker >= workers)
         return 0;
     const int64_t base = quotient(units, workers);
