@@ -100,7 +100,7 @@ struct Cfg {
     static constexpr int TILE_BYTES = BN * D * 2;              // keys or values of a tile
     static constexpr int STAGES = D == 128 ? 4 : 8;
     static constexpr int OUT_BYTES = 32 * 64;                  // staged output of one warp
-    static constexpr int BARRIERS = 2 * STAGES + 18;
+    static constexpr int BARRIERS = 2 * STAGES + 19;
     // shared memory, all of it dynamic: queries, ring, the warps' staging,
     // barriers, TMEM address and abort flag
     static constexpr int RING_AT = 2 * Q_BYTES;
@@ -270,6 +270,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     auto p_ready = [&](int h, int b) { return bar(2 * C::STAGES + 10 + 2 * h + b); };
     auto drain_bar = [&](int h) { return bar(2 * C::STAGES + 14 + h); };
     auto q_free = [&](int h) { return bar(2 * C::STAGES + 16 + h); };
+    const uint32_t part_done = bar(2 * C::STAGES + 18);        // the first item's, by every warp
 
     if (threadIdx.x == 0) {
         prefetch_tensormap(&maps.k);
@@ -289,6 +290,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                 mbar_init(p_ready(h, b), 8);
             }
         }
+        mbar_init(part_done, SOFTMAX_WARPS);
         fence_barrier_init();
         *abort_flag = 0;
     }
@@ -810,17 +812,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                     }
                     if (r < end && part == 0)
                         p.parts.ml[slot_row] = make_float2(m, l);
-                    if (!from_start) {
-                        // either warp's flag also stands for m and l, which one of
-                        // them has written
-                        __threadfence();
-                        __syncwarp();
-                        named_bar_and(pair_bar, 64, true);
-                        if (lane == 0)
-                            st_release_u64(p.parts.flags + worker * 16 + warp,
-                                           p.nonce + (to_end ? 0 : 1));
-                    }
                 }
+            }
+            if (!from_start) {                                 // for the flags behind the part
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(part_done);
             }
             left -= cur.run_units(w, nt);
             if (left > 0)
@@ -833,11 +830,29 @@ __global__ void __launch_bounds__(THREADS, 1)
         // A box of whole tokens and the group's heads: its rows are the half's.
         // Rows behind the sequence's last come along (those of other tokens, or
         // zeros); whatever they hold stays in rows that are never stored.
+        //
+        // This warp also raises the flags behind a part that another worker joins
+        // (the run's first item, if that began in an earlier run): the fence ahead
+        // of them waits two microseconds for the part's stores, which would hold
+        // the softmax warps back.
         uint32_t ph[2] = {0, 0};
         int fetched[2] = {0, 0};
         bool ok = true;
+        uint64_t flag = 0;
+        auto raise_flags = [&]() {
+            ok = wait(part_done, 0u);
+            if (ok) {
+                __threadfence();
+                if (lane < SOFTMAX_WARPS)
+                    st_release_u64(p.parts.flags + worker * SOFTMAX_WARPS + lane, flag);
+            }
+            flag = 0;
+        };
         while (ok && left > 0) {
             const int nt = cur.run_tiles(w, left);
+            const bool due = flag != 0;                        // behind the item before
+            if (cur.tile != cur.t.begin)
+                flag = p.nonce + (cur.tile + nt == cur.t.end ? 0 : 1);
             const int tok = cur.v.q0 + w.by_group(cur.m * w.item_rows);
             for (int h = 0; ok && h < halves_of(); ++h) {
                 ok = wait(q_free(h), ph[h] ^ 1u);
@@ -854,10 +869,14 @@ __global__ void __launch_bounds__(THREADS, 1)
                 }
                 __syncwarp();
             }
+            if (ok && due)
+                raise_flags();
             left -= cur.run_units(w, nt);
             if (left > 0)
                 cur.next_item(w);
         }
+        if (ok && flag != 0)
+            raise_flags();
         // a block that gave up leaves no copy in flight
         if (!ok && elect_one())
             for (int h = 0; h < 2; ++h)
