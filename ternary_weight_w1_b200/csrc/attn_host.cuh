@@ -164,8 +164,16 @@ size_t parts_layout(int64_t workers, int64_t row_cap, int64_t head_dim, bool fla
 
 constexpr int kRowsKernelMax = 32;                   // rows of the rows kernel's largest item
 
-// Workspace: the parts of the rows kernel, then those of the chunk kernel,
-// which only sequences of more rows than the rows kernel's items reach.
+// Rows up to which a sequence is better off in the rows kernel. 32 sequences of
+// 4000 keys, rows kernel / chunk kernel: 32 rows on each of 10 key heads of 64
+// channels 78 / 117 us, 20 rows on each of 5 of 128 channels 114 / 74 us, 32 rows
+// 119 / 74 us, 16 rows 70 / 73 us. Two row tiles of 128 channels are more than a
+// thread's registers hold, and half an item of the chunk kernel keeps up with HBM
+// there. (Four sequences of 32 rows of 64 channels are 46 / 37.)
+constexpr int64_t rows_kernel_rows(int64_t head_dim) { return head_dim == 64 ? 32 : 16; }
+
+// Workspace: the parts of the rows kernel, then those of the chunk kernel, which
+// a call of no more rows than that never reaches.
 struct AttnLayout {
     paged::Parts rows, chunk;
     size_t bytes;
@@ -177,7 +185,7 @@ AttnLayout attn_layout(int64_t rows, int64_t head_dim, char *base)
     const int blocks = head_dim == 64 ? attn::rows::Cfg<64>::BLOCKS : attn::rows::Cfg<128>::BLOCKS;
     l.bytes = parts_layout(kAttnMaxGrid * blocks * attn::rows::WARPS,
                            std::min<int64_t>(rows, kRowsKernelMax), head_dim, false, base, &l.rows);
-    if (rows > kRowsKernelMax)
+    if (rows > rows_kernel_rows(head_dim))
         l.bytes += parts_layout(kAttnMaxGrid, std::min<int64_t>(rows, 2 * attn::chunk::HALF),
                                 head_dim, true, base + l.bytes, &l.chunk);
     return l;
@@ -262,11 +270,19 @@ int run_attn_chunk(attn::Params p, const bitlinear_kv_cache &cache, const Device
     return rc != BITLINEAR_OK ? rc : launch_merge<D>(p, grid, true, dev, st);
 }
 
-// The kernels of a step, by the rows (new tokens times query heads per key
-// head) that its longest sequence can have. Up to 32, only the rows kernel
-// runs. Otherwise sequences of more rows than one of its items go to the chunk
-// kernel, the others to the rows kernel; when the step has at least 64 rows a
-// sequence on average the chunk kernel takes all of them in one launch.
+// The kernels of a step, by the rows (new tokens times query heads per key head)
+// that its longest sequence can have. Few rows, and groups that no half item
+// holds, take the rows kernel. Otherwise the chunk kernel takes all sequences in
+// one launch, or, with 64 channels, only those of more rows than one item of the
+// rows kernel, which takes the others: half an item of 64 channels reads the cache
+// at half of HBM's rate. The second launch pays once there are three sequences
+// and key heads per SM. One chunk and S single tokens behind 500 to 3000 keys, us
+// in one launch / two:
+//   64 channels, 10 heads  S = 31: 69 / 73    S = 63: 127 / 112  S = 127: 210 / 162
+//   64 channels, 16 heads  S = 31: 98 / 84    S = 127: 320 / 210
+//   128 channels, 5 heads  S = 31: 51 / 81    S = 63: 79 / 115   S = 127: 125 / 168
+// With 64 tokens in the chunk; with 1024 (67 rows a sequence on average) and S = 63
+// 186 / 153, with 1500 (191 rows) and S = 31 124 / 121.
 template <int D>
 int run_attention(attn::Params p, const bitlinear_kv_cache &cache, int64_t max_rows, char *ws,
                   const DeviceInfo &dev, cudaStream_t st)
@@ -280,9 +296,10 @@ int run_attention(attn::Params p, const bitlinear_kv_cache &cache, int64_t max_r
     p.parts = layout.rows;
     if (max_rows <= 16)
         return run_attn_rows<D, 1>(p, cache, dev, st);
-    if (max_rows <= kRowsKernelMax || p.work.group > attn::chunk::HALF)
+    if (max_rows <= rows_kernel_rows(D) || p.work.group > attn::chunk::HALF)
         return run_attn_rows<D, 2>(p, cache, dev, st);
-    if (rows < 64 * static_cast<int64_t>(p.work.seqs.seqs)) {
+    const int64_t seqs = p.work.seqs.seqs;
+    if (D == 64 && seqs * p.work.kv_heads >= 3 * dev.sms && rows < 128 * seqs) {
         const bool small = p.work.group <= 16;
         p.work.max_rows = small ? 16 : 32;
         const int rc = small ? run_attn_rows<D, 1>(p, cache, dev, st)

@@ -340,3 +340,26 @@ def test_bad_indexes_are_reported_and_not_used(q):
         assert status == bl.BITLINEAR_ERR_INDEX and word == 2, (what, value, status, word)
         good.check_attention(y, rows=lives)
     assert bl.bitlinear_get_fault() == (bl.BITLINEAR_OK, 0)
+
+
+@pytest.mark.parametrize("window", [0, 100])
+@pytest.mark.parametrize("heads", [(16, 16, 64), (32, 16, 64), (20 * 12, 12, 64)])
+def test_short_and_long_sequences_in_two_launches(heads, window):
+    # enough sequences and key heads of 64 channels that the short ones get a launch
+    # of their own; among them lengths on both sides of its 16 (or 32) rows
+    lens = [(1, 1 + 37 * i % 300) for i in range(34)] + [
+        (8, 90), (9, 90), (16, 16), (17, 500), (0, 7), (32, 40), (33, 33), (130, 200), (1, 0),
+        (2, 64), (3, 1)]
+    lens = lens[::2] + lens[1::2]
+    step = Step(lens, heads, 16, seed=21, spare=3)
+    check(step, window=window)
+    check(step, window=window, max_q_len=130)
+
+
+@pytest.mark.parametrize("window", [0, 70])
+@pytest.mark.parametrize("q,heads", [(17, (2, 2, 128)), (5, (8, 2, 128)), (8, (8, 2, 128)),
+                                     (3, (21, 3, 128)), (1, (40, 2, 128)), (2, (128, 1, 128)),
+                                     (1, (129, 1, 128)), (32, (1, 1, 128))])
+def test_a_few_rows_of_128_channels(q, heads, window):
+    check(Step([(q, q), (q, 1000), (1, 129), (q, 128), (0, 9), (q, q + 63)], heads, 32, seed=22),
+          window=window, max_q_len=q)
