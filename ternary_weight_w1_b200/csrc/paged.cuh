@@ -62,12 +62,12 @@ __device__ __forceinline__ int page_of(const Seqs &q, int s, int c)
 // sequence and key head, where row r is query head r % group of token r / group, so the
 // query heads that share a key head share its tiles. An item takes `full` units
 // per tile of BN keys that any of its rows sees, or `half` when it has no more
-// than half its rows, and `start` units ahead of its first tile's. All units of a launch, items in order and key heads
-// outermost, are dealt to the workers in equal contiguous runs; a tile belongs to
-// the run that it begins in: a long sequence is split wherever a run ends, and a batch
-// of ragged ones stays balanced without the host knowing a length. A worker
-// that gets a whole item writes its output; otherwise it leaves a partial sum
-// that the merge kernel joins in the order of the keys.
+// than half its rows, and `start` units ahead of its first tile's. All units of a
+// launch, items in order and key heads outermost, are dealt to the workers in equal
+// contiguous runs; a tile belongs to the run that it begins in: a long sequence is
+// split wherever a run ends, and a batch of ragged ones stays balanced without the
+// host knowing a length. A worker that gets a whole item writes its output;
+// otherwise it leaves a partial sum that is joined in the order of the keys.
 
 // Division of row numbers by a launch constant: n / d for 0 <= n < 2^31 is the
 // high word of n * mul shifted (mul = ceil(2^(31 + s) / d), s = ceil(log2 d):
@@ -297,10 +297,11 @@ __device__ __forceinline__ int64_t quotient(int64_t n, int64_t d)
 
 // Deals the launch's units: those that worker `worker` has from the first tile
 // that begins in its run, where `cur` is set (none: 0). A run is never shorter
-// than a tile, so that an item's parts lie in successive workers. Every warp of
-// the block calls it (`workers` workers in all); `sums` is shared memory for MAX_GROUPS numbers that must not be used
-// for anything else until the block has met again. Up to 32 sequences every
-// warp counts by itself, without a barrier.
+// than a tile and an item's start, so that an item's parts lie in successive
+// workers. Every warp of the block calls it (`workers` workers in all); `sums` is
+// shared memory for MAX_GROUPS numbers that must not be used for anything else until
+// the block has met again. Up to 32 sequences every warp counts by itself, without
+// a barrier.
 template <int BN>
 __device__ __forceinline__ int64_t deal(const Work &w, int worker, int workers, int64_t *sums,
                                         Cursor<BN> &cur)
