@@ -46,6 +46,7 @@
 #pragma once
 
 #include "attn_rows.cuh"
+#include "f32x2.cuh"
 
 namespace bitlinear {
 namespace attn {

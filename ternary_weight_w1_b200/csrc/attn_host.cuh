@@ -299,7 +299,8 @@ int run_attention(attn::Params p, const bitlinear_kv_cache &cache, int64_t max_r
     if (max_rows <= rows_kernel_rows(D) || p.work.group > attn::chunk::HALF)
         return run_attn_rows<D, 2>(p, cache, dev, st);
     const int64_t seqs = p.work.seqs.seqs;
-    if (D == 64 && seqs * p.work.kv_heads >= 3 * dev.sms && rows < 128 * seqs) {
+    if (D == 64 && p.work.group <= kRowsKernelMax && seqs * p.work.kv_heads >= 3 * dev.sms &&
+        rows < 128 * seqs) {
         const bool small = p.work.group <= 16;
         p.work.max_rows = small ? 16 : 32;
         const int rc = small ? run_attn_rows<D, 1>(p, cache, dev, st)

@@ -16,7 +16,6 @@ __device__ unsigned int g_fault_word;
 enum FaultCode : unsigned int {
     FAULT_NONE = 0,
     FAULT_WAIT_TIMEOUT = 1,
-    FAULT_BAD_INDEX = 2,        // a sequence, length or page index in device memory out of range
 };
 
 // ------------------------------------------------------------------ basics
@@ -224,43 +223,6 @@ __device__ __forceinline__ void drain_wait(uint32_t bar, uint32_t parity, uint64
             return;
         }
     }
-}
-
-// ------------------------------------------------------------ paired fp32
-
-// Two fp32 lanes of one 64-bit register: a multiply-add or an add of both is
-// one instruction.
-__device__ __forceinline__ uint64_t pair(float lo, float hi)
-{
-    uint64_t d;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
-    return d;
-}
-
-__device__ __forceinline__ void unpair(uint64_t v, float &lo, float &hi)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
-{
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
 }
 
 // -------------------------------------------------------------- bulk / TMA

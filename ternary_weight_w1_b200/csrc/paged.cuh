@@ -8,6 +8,11 @@
 #include "common.cuh"
 
 namespace bitlinear {
+
+// Beside FaultCode's bits of the fault word: a sequence, length or page index in
+// device memory out of range.
+constexpr unsigned int FAULT_BAD_INDEX = 2;
+
 namespace paged {
 
 // The step's sequences (see bitlinear_seqs). tokens is the number of query

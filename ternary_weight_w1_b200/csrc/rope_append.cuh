@@ -29,6 +29,7 @@
 #include <cuda_bf16.h>
 
 #include "common.cuh"
+#include "f32x2.cuh"
 #include "paged.cuh"
 
 namespace bitlinear {
