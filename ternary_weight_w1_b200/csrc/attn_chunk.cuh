@@ -38,11 +38,12 @@
 // 18 us of 60 at 2048 tokens of the 2B layer.)
 //
 // One persistent block per SM. Warps 0-7 and 8-15 compute the halves' softmax,
-// warp 16 fetches keys and values through a ring of tiles, warps 17 and 18
-// issue the products of one half each, warp 19 fetches the next item's queries
-// as soon as the last scores of this one are done. A warp whose row's maximum
-// has grown rescales its rows of O_h itself, after the products of the previous
-// step (its o_done).
+// warp 16 fetches keys and values through a ring of tiles, and the next item's
+// queries as soon as the last scores of this one are done, warps 17 and 18 issue the
+// products of one half each. (A warp of its own for the queries made the compiler
+// spill 156 bytes instead of 8: a 2048-token prompt 46.9 us instead of 44.7.) A warp
+// whose row's maximum has grown rescales its rows of O_h itself, after the products
+// of the previous step (its o_done).
 #pragma once
 
 #include "attn_rows.cuh"
@@ -56,7 +57,7 @@ constexpr int HALF = 128;              // most rows of a half item
 constexpr int BN = 128;                // keys of a tile
 constexpr int STEP = 64;               // keys of a step: the tile's two halves
 constexpr int SOFTMAX_WARPS = 16;
-constexpr int THREADS = (SOFTMAX_WARPS + 4) * 32;
+constexpr int THREADS = (SOFTMAX_WARPS + 3) * 32;
 constexpr int TMEM_COLS = 512;
 constexpr int JOIN = 3;                // parts behind its own that a worker joins
 
@@ -333,15 +334,65 @@ __global__ void __launch_bounds__(THREADS, 1)
     paged::PartHeader head[2] = {};
     int64_t left = count;
     if (warp == 16) {
-        // ================================================ keys and values
+        // ======================================= queries, keys and values
+        // An item's queries come between its first keys and the values beside
+        // them: their place is free once the last scores of the item before are
+        // done, when those keys are under way. A box is whole tokens and the group's
+        // heads: its rows are the half's. Rows behind the sequence's last come along
+        // (those of other tokens, or zeros); whatever they hold stays in rows that
+        // are never stored.
+        //
+        // This warp also raises the flags behind a part that another worker joins
+        // (the run's first item, if that began in an earlier run): the fence ahead
+        // of them waits two microseconds for the part's stores, which would hold
+        // the softmax warps back. It does so when two tiles of the next item are in
+        // the ring.
         const int page = 1 << w.seqs.page_shift;
         const int box = min(page, BN), subs = BN / box, boxes = subs * C::CH;
         int st = 0;
         uint32_t ph = 0, armed = 0;                            // armed: stages in flight, as bits
+        uint32_t q_ph[2] = {0, 0};
+        int fetched[2] = {0, 0};
+        uint64_t flag = 0;
         bool ok = true;
+        auto raise_flags = [&]() {
+            ok = wait(part_done, 0u);
+            if (ok) {
+                __threadfence();
+                if (lane < SOFTMAX_WARPS)
+                    st_release_u64(p.parts.flags + worker * SOFTMAX_WARPS + lane, flag);
+            }
+            flag = 0;
+        };
+        auto fetch_queries = [&]() {
+            const int tok = cur.v.q0 + w.by_group(cur.m * w.item_rows);
+            for (int h = 0; ok && h < halves_of(); ++h) {
+                ok = wait(q_free(h), q_ph[h] ^ 1u);
+                if (!ok)
+                    break;
+                q_ph[h] ^= 1u;
+                fetched[h] = 1;
+                if (elect_one()) {
+                    mbar_arrive_expect_tx(q_ready(h), half_rows * D * 2);
+                    for (int c = 0; c < C::CH; ++c)
+                        tma_load_3d(q_smem + h * C::Q_BYTES + c * (HALF * 128), &q_map, c * 64,
+                                    cur.h * w.group, tok + h * w.by_group(half_rows),
+                                    q_ready(h));
+                }
+                __syncwarp();
+            }
+        };
         while (ok && left > 0) {
             const int nt = cur.run_tiles(w, left);
+            const bool due = flag != 0;                        // behind the item before
+            if (cur.tile != cur.t.begin)
+                flag = p.nonce + (cur.tile + nt == cur.t.end ? 0 : 1);
             for (int j = 0; ok && j < nt; ++j) {
+                if (j == 2 && due) {
+                    raise_flags();
+                    if (!ok)
+                        break;
+                }
                 const int sub = lane % subs, ch = (lane / subs) % C::CH;
                 const int key = (cur.tile + j) * BN + sub * box;
                 // a box without a needed key, or of a page that the table does
@@ -352,7 +403,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                     if (id >= 0)
                         row = ((id * w.kv_heads + cur.h) << w.seqs.page_shift) + (key & (page - 1));
                 }
-                for (int kv = 0; kv < 2; ++kv) {
+                for (int kv = 0; ok && kv < 2; ++kv) {
                     if (!wait(empty(st), ph ^ 1u)) {
                         ok = false;
                         break;
@@ -368,18 +419,29 @@ __global__ void __launch_bounds__(THREADS, 1)
                         st = 0;
                         ph ^= 1u;
                     }
+                    if (j == 0 && kv == 0)
+                        fetch_queries();
                 }
             }
+            if (ok && due && flag != 0)
+                raise_flags();
             left -= cur.run_units(w, nt);
             if (ok && left > 0)
                 cur.next_item(w);
         }
+        if (ok && flag != 0)
+            raise_flags();
         // a block that gave up leaves no copy in flight: a stage's last phase
         // is the one before its next fill
-        if (!ok && lane == 0)
+        if (!ok && lane == 0) {
             for (int s = 0; s < C::STAGES; ++s)
                 if ((armed >> s) & 1u)
                     drain_wait(full(s), s < st ? ph : ph ^ 1u, p.wait_limit_ns);
+            for (int h = 0; h < 2; ++h)
+                if (fetched[h])
+                    drain_wait(q_ready(h), q_ph[h] ^ 1u, p.wait_limit_ns);
+        }
+        __syncwarp();
     } else if (warp == 17 || warp == 18) {
         // ============================================== products of half h
         constexpr uint32_t S_IDESC = idesc_bf16(HALF, STEP, false);
@@ -508,7 +570,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             drain_wait(drain_bar(h), 0u, p.wait_limit_ns);
         }
         __syncwarp();
-    } else if (warp < SOFTMAX_WARPS) {
+    } else {
         // ======================================================== softmax
         const int h = warp >> 3;                               // half of the item
         const int part = (warp >> 2) & 1;                      // 32 of the step's 64 keys
@@ -826,64 +888,6 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (!ok)
             head[0].rows = head[1].rows = 0;                 // no part that could be merged
-    } else {
-        // ======================================================== queries
-        // A box of whole tokens and the group's heads: its rows are the half's.
-        // Rows behind the sequence's last come along (those of other tokens, or
-        // zeros); whatever they hold stays in rows that are never stored.
-        //
-        // This warp also raises the flags behind a part that another worker joins
-        // (the run's first item, if that began in an earlier run): the fence ahead
-        // of them waits two microseconds for the part's stores, which would hold
-        // the softmax warps back.
-        uint32_t ph[2] = {0, 0};
-        int fetched[2] = {0, 0};
-        bool ok = true;
-        uint64_t flag = 0;
-        auto raise_flags = [&]() {
-            ok = wait(part_done, 0u);
-            if (ok) {
-                __threadfence();
-                if (lane < SOFTMAX_WARPS)
-                    st_release_u64(p.parts.flags + worker * SOFTMAX_WARPS + lane, flag);
-            }
-            flag = 0;
-        };
-        while (ok && left > 0) {
-            const int nt = cur.run_tiles(w, left);
-            const bool due = flag != 0;                        // behind the item before
-            if (cur.tile != cur.t.begin)
-                flag = p.nonce + (cur.tile + nt == cur.t.end ? 0 : 1);
-            const int tok = cur.v.q0 + w.by_group(cur.m * w.item_rows);
-            for (int h = 0; ok && h < halves_of(); ++h) {
-                ok = wait(q_free(h), ph[h] ^ 1u);
-                if (!ok)
-                    break;
-                ph[h] ^= 1u;
-                fetched[h] = 1;
-                if (elect_one()) {
-                    mbar_arrive_expect_tx(q_ready(h), half_rows * D * 2);
-                    for (int c = 0; c < C::CH; ++c)
-                        tma_load_3d(q_smem + h * C::Q_BYTES + c * (HALF * 128), &q_map, c * 64,
-                                    cur.h * w.group, tok + h * w.by_group(half_rows),
-                                    q_ready(h));
-                }
-                __syncwarp();
-            }
-            if (ok && due)
-                raise_flags();
-            left -= cur.run_units(w, nt);
-            if (left > 0)
-                cur.next_item(w);
-        }
-        if (ok && flag != 0)
-            raise_flags();
-        // a block that gave up leaves no copy in flight
-        if (!ok && elect_one())
-            for (int h = 0; h < 2; ++h)
-                if (fetched[h])
-                    drain_wait(q_ready(h), ph[h] ^ 1u, p.wait_limit_ns);
-        __syncwarp();
     }
     tc_fence_before_sync();
     __syncthreads();
