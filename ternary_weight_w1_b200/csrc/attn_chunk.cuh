@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     // Whether no row of the item sees the first, or the last, step of its tiles in
     // this run. Such a step passes its barriers, but nothing is computed; one step
     // of an item is always left. Only with 64 channels, where windowed prompts take
-    // 207 us instead of 220: with 128 the code spills 144 bytes more and a 2048-token
+    // 205 us instead of 218: with 128 the code spills 144 bytes more and a 2048-token
     // prompt takes 47.2 us instead of 44.6.
     constexpr bool SKIP = D == 64;
     auto unseen_first = [&]() { return SKIP && cur.tile * BN + STEP <= cur.t.klo; };
