@@ -363,3 +363,38 @@ def test_short_and_long_sequences_in_two_launches(heads, window):
 def test_a_few_rows_of_128_channels(q, heads, window):
     check(Step([(q, q), (q, 1000), (1, 129), (q, 128), (0, 9), (q, q + 63)], heads, 32, seed=22),
           window=window, max_q_len=q)
+
+
+@pytest.mark.parametrize("kv", [64, 65, 127, 128, 129, 191, 192, 193, 449])
+@pytest.mark.parametrize("window", [0, 1, 63, 64, 65, 128])
+def test_ends_and_windows_about_the_steps_of_sixty_four_keys(kv, window):
+    # first and last steps that hold one key, all keys or none that a row sees
+    for heads in ((4, 1, 64), (2, 2, 64), (4, 1, 128)):
+        check(Step([(kv, kv), (33, kv), (min(kv, 200), kv + 64)], heads, 16, seed=kv), window=window)
+
+
+def test_prompts_on_two_streams():
+    # both fill the GPU and join split items while the other one's blocks come and go
+    steps = [Step([(700, 900), (300, 1500)], (20, 5, 128), 64, seed=31),
+             Step([(900, 900), (1, 3000), (250, 2000)], (40, 10, 64), 16, seed=32)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[], []]
+    for _ in range(10):
+        for i in (0, 1):
+            outs[i].append(steps[i].attend(stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        steps[i].check_attention(outs[i][0])
+        assert all(torch.equal(o.view(torch.int16), outs[i][0].view(torch.int16)) for o in outs[i])
+
+
+@pytest.mark.parametrize("q", [2, 100])
+def test_starts_that_fall_are_reported(q):
+    # sequences that overlap write the same rows: nothing out of range, and a fault
+    step = Step([(q, 150), (q, 150), (q, 150)], (8, 2, 64), 16, seed=33)
+    step.q_start[2] = 0
+    y = step.attend()
+    torch.cuda.synchronize()
+    assert bl.bitlinear_get_fault()[0] == bl.BITLINEAR_ERR_INDEX
+    assert torch.isfinite(y).all()
