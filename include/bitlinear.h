@@ -530,7 +530,8 @@ typedef struct {
  * At most 16384 sequences. A value that points outside the rows, the table or
  * the cache is never used for an access: bitlinear_get_fault reports it
  * (BITLINEAR_ERR_INDEX), a key on such a page counts as zeros, a token that
- * belongs there is not stored, and the results of that sequence are otherwise
+ * belongs there is not stored, no token of a sequence is whose q_start or
+ * kv_len is such a value, and the results of that sequence are otherwise
  * unspecified. */
 typedef struct {
     const int32_t *q_start_dev, *kv_len_dev, *page_table_dev;

@@ -36,16 +36,23 @@ struct View {
     int q0, qlen, kv;
 };
 
-// Sequence s, cut to the rows and the page slots that exist (a value outside
-// them is recorded as a fault).
-__device__ __forceinline__ View view(const Seqs &q, int s)
+// Sequence s, cut to the rows and the page slots that exist. False when a value
+// lay outside them.
+__device__ __forceinline__ bool read_view(const Seqs &q, int s, View &v)
 {
     const int b = __ldg(q.q_start + s), e = __ldg(q.q_start + s + 1), n = __ldg(q.kv_len + s);
-    View v;
     v.q0 = min(max(b, 0), q.tokens);
     v.qlen = min(max(e, v.q0), q.tokens) - v.q0;
     v.kv = min(max(n, 0), q.table_cols << q.page_shift);
-    if (v.q0 != b || v.q0 + v.qlen != e || v.kv != n)
+    return v.q0 == b && v.q0 + v.qlen == e && v.kv == n;
+}
+
+// The same for reading, where the cut sequence will do; a value outside is recorded
+// as a fault.
+__device__ __forceinline__ View view(const Seqs &q, int s)
+{
+    View v;
+    if (!read_view(q, s, v))
         fault_index();
     return v;
 }

@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(THREADS) rope_append_kernel(const Params p)
     __shared__ __align__(16) float gains[2][D];         // of the queries, of the keys
     __shared__ uint4 staged[STAGES][2][THREADS];        // a thread's own next units
     __shared__ int64_t slot[MAX_ROWS];      // a row's first element in the caches, -1: none
-    __shared__ int posn[MAX_ROWS];          // a row's position, -1: no row of a sequence
+    __shared__ int posn[MAX_ROWS];          // a row's position, -1: none
 
     pdl_wait();
     pdl_launch_dependents();
@@ -150,9 +150,14 @@ __global__ void __launch_bounds__(THREADS) rope_append_kernel(const Params p)
             int pos = -1;
             int64_t at = -1;
             if (s >= 0) {
-                const paged::View v = paged::view(p.seqs, s);
-                // a row before position 0 has no place
-                pos = max(v.kv - (v.q0 + v.qlen - t), -1);
+                // A row before position 0 has no place. Nor has any row of a sequence
+                // with a value out of range: cut to what exists, it would put the
+                // row in another token's.
+                paged::View v;
+                if (paged::read_view(p.seqs, s, v))
+                    pos = max(v.kv - (v.q0 + v.qlen - t), -1);
+                else
+                    paged::fault_index();
             }
             if (pos >= 0) {
                 const int page = paged::page_of(p.seqs, s, pos >> p.seqs.page_shift);

@@ -147,3 +147,39 @@ def test_bad_indexes_are_reported_and_not_used():
             changed = (step.k_cache.view(torch.int16) != kept.view(torch.int16)).any(-1).any(1)
             assert changed.sum() == 2
     assert bl.bitlinear_get_fault() == (bl.BITLINEAR_OK, 0)
+
+
+@pytest.mark.parametrize("bad", ["one token more than the table holds", "far behind the table",
+                                 "most negative", "end behind the rows", "start before the rows"])
+@pytest.mark.parametrize("page", [16, 64])
+def test_a_sequence_of_bad_lengths_stores_nothing(bad, page):
+    # every column of the table holds a page of the cache, so that a length cut to
+    # what exists would find a place: nothing may be stored there
+    step = Step([(3, 3 * page), (2, 3 * page), (4, 2 * page + 5)], (4, 2, 64), page, seed=10,
+                extra_cols=0)
+    f = frequencies(64)
+    want = [c.clone() for c in (step.k_cache, step.v_cache)]
+    good = Step([(3, 3 * page), (2, 3 * page), (4, 2 * page + 5)], (4, 2, 64), page, seed=10,
+                extra_cols=0)
+    good.append(f)
+    stored = {0: 3, 1: 2, 2: 4}
+    if bad == "end behind the rows":
+        step.q_start[3] = 10 ** 6
+        del stored[2]
+    elif bad == "start before the rows":
+        step.q_start[0] = -7
+        del stored[0]
+    else:
+        step.kv_len[1] = {"one token more than the table holds": 3 * page + 1,
+                          "far behind the table": 2 ** 31 - 1, "most negative": -2 ** 31}[bad]
+        del stored[1]
+    for s, n in stored.items():                        # what the good sequences store
+        kv = step.lens[s][1]
+        pos = torch.arange(kv - n, kv, device="cuda")
+        at, slot = good.table[s].long()[pos // page], pos % page
+        for w, c in zip(want, (good.k_cache, good.v_cache)):
+            w[at, :, slot] = c[at, :, slot]
+    step.append(f)
+    assert bl.bitlinear_get_fault() == (bl.BITLINEAR_ERR_INDEX, 2)
+    for c, w in zip((step.k_cache, step.v_cache), want):
+        assert (c.view(torch.int16) != w.view(torch.int16)).sum().item() == 0
