@@ -308,8 +308,12 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int worker = blockIdx.x;
     Cursor cur;
     const int64_t count = paged::deal<BN>(w, worker, gridDim.x, sums, cur);
-    if (w.seqs.seqs > 32)
-        __syncthreads();                                       // sums is read; its memory is Q's
+    if (w.seqs.seqs > 32) {
+        // sums is read; its memory is Q's, which TMA writes: a barrier alone does not
+        // order these accesses before those of the other proxy
+        fence_proxy_async();
+        __syncthreads();
+    }
 
     // The whole warp waits; false after a timeout anywhere in the block.
     auto wait = [&](uint32_t b, uint32_t parity) {

@@ -398,3 +398,15 @@ def test_starts_that_fall_are_reported(q):
     torch.cuda.synchronize()
     assert bl.bitlinear_get_fault()[0] == bl.BITLINEAR_ERR_INDEX
     assert torch.isfinite(y).all()
+
+
+@pytest.mark.parametrize("heads", [(8, 2, 128), (8, 2, 64)])
+@pytest.mark.parametrize("n", [32, 33, 65, 600])
+def test_chunks_among_many_sequences(n, heads):
+    # above 32 sequences the deal's sums stand in shared memory that the first
+    # queries are copied to
+    lens = [(1 + 89 * i % 40, 40 + 53 * i % 90) for i in range(n)]
+    step = Step(lens, heads, 16, seed=34)
+    y, _ = check(step)
+    for _ in range(3):
+        assert torch.equal(step.attend().view(torch.int16), y.view(torch.int16))
