@@ -33,9 +33,11 @@
 // adds the parts to its own, in the order of the keys, before it writes the
 // output. The flags hold the launch's number, so their memory needs no
 // initialisation; the kernel behind this one, which joins items of more parts,
-// clears them. Blocks wait only for blocks of a higher number, which are never
-// kept from running by them. (Leaving every part to a kernel of its own took
-// 18 us of 60 at 2048 tokens of the 2B layer.)
+// clears them. Runs are numbered from the last block to the first, so that a block
+// waits only for blocks of a lower number. The GPU starts blocks in the order of
+// their numbers: what is waited for runs already or is done, however few SMs other
+// work leaves to the launch. (Leaving every part to a kernel of its own took 18 us
+// of 60 at 2048 tokens of the 2B layer.)
 //
 // One persistent block per SM. Warps 0-7 and 8-15 compute the halves' softmax,
 // warp 16 fetches keys and values through a ring of tiles, and the next item's
@@ -60,6 +62,9 @@ constexpr int SOFTMAX_WARPS = 16;
 constexpr int THREADS = (SOFTMAX_WARPS + 3) * 32;
 constexpr int TMEM_COLS = 512;
 constexpr int JOIN = 3;                // parts behind its own that a worker joins
+
+// The worker (the run of units) of a block. Workers wait for the JOIN next ones.
+__host__ __device__ constexpr int worker_of(int block, int blocks) { return blocks - 1 - block; }
 
 __device__ __forceinline__ uint64_t ld_acquire_u64(const uint64_t *p)
 {
@@ -305,7 +310,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     pdl_wait();
     pdl_launch_dependents();
     const paged::Work &w = p.work;
-    const int worker = blockIdx.x;
+    const int worker = worker_of(blockIdx.x, gridDim.x);
     Cursor cur;
     const int64_t count = paged::deal<BN>(w, worker, gridDim.x, sums, cur);
     if (w.seqs.seqs > 32) {

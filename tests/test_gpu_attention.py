@@ -410,3 +410,23 @@ def test_chunks_among_many_sequences(n, heads):
     y, _ = check(step)
     for _ in range(3):
         assert torch.equal(step.attend().view(torch.int16), y.view(torch.int16))
+
+
+def test_prompts_on_many_streams_beside_decoding():
+    # blocks that join parts hold their SMs while the other launches, of both
+    # kernels and two priorities, take those that come free
+    steps = [Step([(500 + 90 * i, 700 + 200 * i), (60, 900)], heads, 64, seed=40 + i)
+             for i, heads in enumerate([(20, 5, 128), (8, 2, 64), (8, 1, 128)])]
+    steps += [Step([(1, 20000), (1, 9000)], (8, 2, 128), 128, seed=44),
+              Step([(1, 30000)], (8, 2, 64), 64, seed=45)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(priority=-(i % 2)) for i in range(len(steps))]
+    outs = [[] for _ in steps]
+    for _ in range(12):
+        for s, st, o in zip(steps, streams, outs):
+            o.append(s.attend(stream=st))
+    torch.cuda.synchronize()
+    assert bl.bitlinear_get_fault() == (bl.BITLINEAR_OK, 0)
+    for s, o in zip(steps, outs):
+        s.check_attention(o[0])
+        assert all(torch.equal(x.view(torch.int16), o[0].view(torch.int16)) for x in o)
