@@ -66,6 +66,16 @@ constexpr int JOIN = 3;                // parts behind its own that a worker joi
 // The worker (the run of units) of a block. Workers wait for the JOIN next ones.
 __host__ __device__ constexpr int worker_of(int block, int blocks) { return blocks - 1 - block; }
 
+// Limit of a wait for another worker's part. Runs are equal and the other one's block
+// started no later, but its SM may be slower (it shares it with other work), so it is
+// late by a part of the run's own time, which has no limit: `base_ns`, as for the waits
+// inside a block, and ten times the 0.45 us that a unit takes, up to a minute.
+// `units`: an upper bound of a run's.
+__host__ __device__ constexpr uint64_t join_wait_ns(uint64_t base_ns, double units)
+{
+    return base_ns + static_cast<uint64_t>(units < 60e9 / 4500.0 ? units * 4500.0 : 60e9);
+}
+
 __device__ __forceinline__ uint64_t ld_acquire_u64(const uint64_t *p)
 {
     uint64_t v;
@@ -793,7 +803,7 @@ __global__ void __launch_bounds__(THREADS, 1)
                             break;
                         if (lane == 0)
                             flag = wait_flag(p.parts.flags + (worker + 1 + k) * 16 + warp, p.nonce,
-                                         abort_flag, p.wait_limit_ns);
+                                         abort_flag, p.join_limit_ns);
                         flag = __shfl_sync(0xffffffffu, flag, 0);
                         ok = named_bar_and(pair_bar, 64, flag != 0);
                         if (!ok)

@@ -262,6 +262,13 @@ int run_attn_chunk(attn::Params p, const bitlinear_kv_cache &cache, const Device
         !make_map_cache(&maps.v, cache.v_dev, cache, box))
         return BITLINEAR_ERR_CUDA;
     const int grid = std::min(dev.sms, kAttnMaxGrid);
+    // at most so many items, of so many tiles (the lengths are known on the device only)
+    const double items = (static_cast<double>(p.work.seqs.tokens) / (2 * tokens) +
+                          static_cast<double>(p.work.seqs.seqs)) * p.work.kv_heads;
+    const double keys = static_cast<double>(p.work.seqs.table_cols) * cache.page;
+    const double seen = p.work.window > 0 ? std::min(keys, p.work.window + 2.0 * tokens) : keys;
+    const double units = items * ((seen / attn::chunk::BN + 2) * p.work.full + p.work.start);
+    p.join_limit_ns = attn::chunk::join_wait_ns(p.wait_limit_ns, units / grid);
     cudaError_t e = allow_smem<attn::chunk::attn_chunk_kernel<D>>(dev.id, smem);
     if (e == cudaSuccess)
         e = launch(attn::chunk::attn_chunk_kernel<D>, dim3(grid), dim3(attn::chunk::THREADS),

@@ -78,6 +78,7 @@ struct Params {
     paged::Work work;
     paged::Parts parts;
     uint64_t wait_limit_ns;
+    uint64_t join_limit_ns;    // of the chunk kernel's waits for other blocks
     uint64_t nonce;            // even, another for every launch
 };
 

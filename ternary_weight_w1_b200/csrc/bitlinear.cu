@@ -48,7 +48,7 @@ constexpr double kSplitMinSavedBlocks = 10.0;
 constexpr int64_t kSplitMinCtaBlocks = 8;
 // k-blocks of 256 per CTA from which the small token tiles take 512-k stages
 constexpr int64_t kDeepStageMinBlocks = 8;
-constexpr uint64_t kWaitLimitNs = 1000000000ull;  // 1 s: far above any legitimate wait
+constexpr uint64_t kWaitLimitNs = 1000000000ull;  // 1 s: far above any legitimate wait in a block
 constexpr int kMaxDevices = 64;
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }

@@ -18,6 +18,10 @@ int main()
         for (int b = 0; b < blocks; ++b)
             std::printf(" %d", chunk::worker_of(b, blocks));
     std::printf("\\n");
+    for (double units : {0.0, 100.0, 2.3e6, 1e12})
+        std::printf("%llu ", static_cast<unsigned long long>(
+                                 chunk::join_wait_ns(1000000000ull, units)));
+    std::printf("\\n");
 }
 """
 
@@ -48,3 +52,12 @@ def test_blocks_wait_only_for_blocks_that_start_before_them(output):
             for other in range(w + 1, min(w + 1 + join, blocks)):
                 assert block[other] < block[w], (blocks, w, other)
     assert at == len(workers)
+
+
+def test_waits_for_other_blocks_are_limited_by_the_work_of_a_launch(output):
+    # a run of 32768 rows of 8 key heads behind a million keys is 2.3 million units, of
+    # 0.45 us each: blocks a second apart are sound there
+    none, few, long, most = map(int, output[1].split())
+    assert none == 10 ** 9 and none < few < none + 10 ** 6
+    assert long >= 10 ** 9 + 5 * 2.3e6 * 450
+    assert most == 61 * 10 ** 9
