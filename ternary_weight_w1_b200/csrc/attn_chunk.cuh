@@ -461,9 +461,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         if (ok && flag != 0)
             raise_flags();
-        // a block that gave up leaves no copy in flight: a stage's last phase
-        // is the one before its next fill
-        if (!ok && lane == 0) {
+        // No copy is left in flight when the block ends, whichever of its warps gave up
+        // (this one may be done when another does): a stage's last phase is the one
+        // before its next fill.
+        if (lane == 0) {
             for (int s = 0; s < C::STAGES; ++s)
                 if ((armed >> s) & 1u)
                     drain_wait(full(s), s < st ? ph : ph ^ 1u, p.wait_limit_ns);
