@@ -602,7 +602,9 @@ size_t bitlinear_workspace_bytes_attention(int64_t tokens, int64_t seqs,
  * Scores, maxima, sums and the output are fp32; the weights of the sum over
  * the values are rounded to bf16 for the tensor cores. Queries, and keys and
  * values at the positions that a sequence's rows see, are finite; the other
- * slots of its pages may hold anything. Repeated calls give the same bits. */
+ * slots of its pages may hold anything. Repeated calls give the same bits.
+ * When a wait runs out (bitlinear_get_fault), a row's output of a head is either
+ * complete or not written; the next call may use the same workspace. */
 int bitlinear_paged_attention(const void *q_dev, int64_t q_stride,
                               int64_t tokens, int64_t q_heads,
                               const bitlinear_kv_cache *cache,
@@ -695,6 +697,20 @@ int bitlinear_forward_inject_timeout(const void *x_dev, bitlinear_dtype xdt,
                                      size_t workspace_bytes,
                                      void *cuda_stream, int path,
                                      int timeout_us);
+
+/* bitlinear_paged_attention with one wait made to run out likewise: worker
+ * `worker` (>= 0; of a launch of the kernel for few rows per sequence one warp,
+ * of the other one block) waits for its first tile of keys on a barrier that
+ * expects an arrival more than there is, and every wait gives up after timeout_us
+ * microseconds, in [1, 10^7]. That worker, and workers that wait for it, record a
+ * fault and return; see bitlinear_paged_attention for what is written then. A
+ * worker without work makes no difference. */
+int bitlinear_paged_attention_inject_timeout(
+    const void *q_dev, int64_t q_stride, int64_t tokens, int64_t q_heads,
+    const bitlinear_kv_cache *cache, const bitlinear_seqs *seqs, float scale,
+    int64_t window, int64_t max_q_len, void *y_dev, int64_t y_stride,
+    float *lse_dev_or_null, void *workspace_dev, size_t workspace_bytes,
+    void *cuda_stream, int worker, int timeout_us);
 
 #ifdef __cplusplus
 }

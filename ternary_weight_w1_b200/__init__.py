@@ -77,6 +77,7 @@ EXPORTS = (
     "bitlinear_paged_attention",
     "bitlinear_workspace_bytes_attn",
     "bitlinear_attn_forward",
+    "bitlinear_paged_attention_inject_timeout",
 )
 
 
@@ -174,6 +175,9 @@ def lib() -> ctypes.CDLL:
         L.bitlinear_paged_attention.restype = ctypes.c_int
         L.bitlinear_paged_attention.argtypes = [p, i64, i64, i64, p, p, f32, i64, i64, p, i64, p,
                                                 p, sz, p]
+        L.bitlinear_paged_attention_inject_timeout.restype = ctypes.c_int
+        L.bitlinear_paged_attention_inject_timeout.argtypes = (
+            L.bitlinear_paged_attention.argtypes + [ctypes.c_int, ctypes.c_int])
         L.bitlinear_workspace_bytes_attn.restype = sz
         L.bitlinear_workspace_bytes_attn.argtypes = [i64] * 6
         L.bitlinear_attn_forward.restype = ctypes.c_int
@@ -693,21 +697,41 @@ def bitlinear_paged_attention(q, k_cache, v_cache, q_start, kv_len, page_table, 
                                  max_q_len, y, lse, workspace,
                                  None if stream is None else stream.cuda_stream)
     if rc is None:
-        import torch
-        a = _Args()
-        _, D, _, cache, seqs = _paged(a, k_cache, v_cache, q_start, kv_len, page_table)
-        qp, qs, heads = a.rows(q, "q", None, D)
-        T = q.shape[0]
-        _same_rows(y, "y", T)
-        yp, ys, _ = a.rows(y, "y", heads, D)
-        rc = lib().bitlinear_paged_attention(
-            qp, qs, T, heads, cache, seqs, float(D ** -0.5 if scale is None else scale),
-            int(window), int(max_q_len or 0), yp, ys,
-            a.ptr(lse, "lse", torch.float32, (T, heads)),
-            a.ptr(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
+        rc = lib().bitlinear_paged_attention(*_attention_args(
+            q, k_cache, v_cache, q_start, kv_len, page_table, scale, window, max_q_len, y, lse,
+            workspace, stream))
     if rc:
         _check(rc, "bitlinear_paged_attention")
     return y
+
+
+def bitlinear_paged_attention_inject_timeout(q, k_cache, v_cache, q_start, kv_len, page_table,
+                                             worker: int, timeout_us: int, scale=None,
+                                             window: int = 0, max_q_len: int | None = None, *, y,
+                                             lse=None, workspace=None, stream=None) -> int:
+    """bitlinear_paged_attention with worker ``worker`` waiting in vain for its first
+    tile of keys and every wait limited to ``timeout_us``; returns the status that
+    the launch reported (the fault is read by bitlinear_get_fault)."""
+    if workspace is None:
+        workspace = _attention_workspace(q, k_cache, page_table, stream)
+    return int(lib().bitlinear_paged_attention_inject_timeout(
+        *_attention_args(q, k_cache, v_cache, q_start, kv_len, page_table, scale, window,
+                         max_q_len, y, lse, workspace, stream), int(worker), int(timeout_us)))
+
+
+def _attention_args(q, k_cache, v_cache, q_start, kv_len, page_table, scale, window, max_q_len, y,
+                    lse, workspace, stream):
+    """The library's arguments of an attention call, checked."""
+    import torch
+    a = _Args()
+    _, D, _, cache, seqs = _paged(a, k_cache, v_cache, q_start, kv_len, page_table)
+    qp, qs, heads = a.rows(q, "q", None, D)
+    T = q.shape[0]
+    _same_rows(y, "y", T)
+    yp, ys, _ = a.rows(y, "y", heads, D)
+    return (qp, qs, T, heads, cache, seqs, float(D ** -0.5 if scale is None else scale),
+            int(window), int(max_q_len or 0), yp, ys, a.ptr(lse, "lse", torch.float32, (T, heads)),
+            a.ptr(workspace, "workspace", torch.uint8), workspace.numel(), _stream(stream))
 
 
 def _attention_workspace(q, k_cache, page_table, stream):

@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         prefetch_tensormap(&maps.v);
         prefetch_tensormap(&q_map);
         for (int s = 0; s < C::STAGES; ++s) {
-            mbar_init(full(s), 1);
+            mbar_init(full(s), 1 + (s == 0 && worker_of(blockIdx.x, gridDim.x) == p.stuck));
             mbar_init(empty(s), 2);                            // both halves
         }
         for (int h = 0; h < 2; ++h) {

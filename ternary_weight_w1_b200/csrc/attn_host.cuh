@@ -297,7 +297,6 @@ int run_attention(attn::Params p, const bitlinear_kv_cache &cache, int64_t max_r
     const int64_t rows = static_cast<int64_t>(p.work.seqs.tokens) * p.work.group;
     const AttnLayout layout = attn_layout(rows, D, ws);
     p.cache_rows = static_cast<int>(cache.pages * cache.kv_heads * cache.page);
-    p.wait_limit_ns = kWaitLimitNs;
     p.work.min_rows = 1;
     p.work.max_rows = INT_MAX;
     p.parts = layout.rows;
@@ -401,12 +400,13 @@ extern "C" size_t bitlinear_workspace_bytes_attention(int64_t tokens, int64_t se
     return attn_layout(tokens * (q_heads / kv_heads), head_dim, nullptr).bytes;
 }
 
-extern "C" int bitlinear_paged_attention(const void *q_dev, int64_t q_stride, int64_t tokens,
-                                         int64_t q_heads, const bitlinear_kv_cache *cache,
-                                         const bitlinear_seqs *seqs, float scale, int64_t window,
-                                         int64_t max_q_len, void *y_dev, int64_t y_stride,
-                                         float *lse_dev_or_null, void *workspace_dev,
-                                         size_t workspace_bytes, void *cuda_stream)
+namespace {
+
+int paged_attention_impl(const void *q_dev, int64_t q_stride, int64_t tokens, int64_t q_heads,
+                         const bitlinear_kv_cache *cache, const bitlinear_seqs *seqs, float scale,
+                         int64_t window, int64_t max_q_len, void *y_dev, int64_t y_stride,
+                         float *lse_dev_or_null, void *workspace_dev, size_t workspace_bytes,
+                         void *cuda_stream, int stuck, uint64_t wait_limit_ns)
 {
     bool empty = false;
     int rc = check_paged(tokens, q_heads, cache, seqs, &empty);
@@ -447,11 +447,41 @@ extern "C" int bitlinear_paged_attention(const void *q_dev, int64_t q_stride, in
     p.work.group = static_cast<int>(q_heads / cache->kv_heads);
     p.work.by_group = divide_by(p.work.group);
     p.work.window = static_cast<int>(std::min(window, kAttnMaxKeys));
+    p.wait_limit_ns = wait_limit_ns;
+    p.stuck = stuck;
     const int64_t longest = max_q_len > 0 ? std::min(max_q_len, tokens) : tokens;
     cudaStream_t st = static_cast<cudaStream_t>(cuda_stream);
     char *ws = static_cast<char *>(workspace_dev);
     return D == 64 ? run_attention<64>(p, *cache, longest * p.work.group, ws, *dev, st)
                    : run_attention<128>(p, *cache, longest * p.work.group, ws, *dev, st);
+}
+
+}  // namespace
+
+extern "C" int bitlinear_paged_attention(const void *q_dev, int64_t q_stride, int64_t tokens,
+                                         int64_t q_heads, const bitlinear_kv_cache *cache,
+                                         const bitlinear_seqs *seqs, float scale, int64_t window,
+                                         int64_t max_q_len, void *y_dev, int64_t y_stride,
+                                         float *lse_dev_or_null, void *workspace_dev,
+                                         size_t workspace_bytes, void *cuda_stream)
+{
+    return paged_attention_impl(q_dev, q_stride, tokens, q_heads, cache, seqs, scale, window,
+                                max_q_len, y_dev, y_stride, lse_dev_or_null, workspace_dev,
+                                workspace_bytes, cuda_stream, -1, kWaitLimitNs);
+}
+
+extern "C" int bitlinear_paged_attention_inject_timeout(
+    const void *q_dev, int64_t q_stride, int64_t tokens, int64_t q_heads,
+    const bitlinear_kv_cache *cache, const bitlinear_seqs *seqs, float scale, int64_t window,
+    int64_t max_q_len, void *y_dev, int64_t y_stride, float *lse_dev_or_null, void *workspace_dev,
+    size_t workspace_bytes, void *cuda_stream, int worker, int timeout_us)
+{
+    if (worker < 0 || timeout_us < 1 || timeout_us > 10 * 1000 * 1000)
+        return BITLINEAR_ERR_ARG;
+    return paged_attention_impl(q_dev, q_stride, tokens, q_heads, cache, seqs, scale, window,
+                                max_q_len, y_dev, y_stride, lse_dev_or_null, workspace_dev,
+                                workspace_bytes, cuda_stream, worker,
+                                static_cast<uint64_t>(timeout_us) * 1000ull);
 }
 
 // ---------------------------------------------------------- attention block

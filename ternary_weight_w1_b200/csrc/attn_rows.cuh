@@ -79,6 +79,7 @@ struct Params {
     paged::Parts parts;
     uint64_t wait_limit_ns;
     uint64_t join_limit_ns;    // of the chunk kernel's waits for other blocks
+    int stuck;                 // worker whose first stage never fills (a test), or -1
     uint64_t nonce;            // even, another for every launch
 };
 
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(THREADS, Cfg<D>::BLOCKS)
     }
     if (lane == 0) {
         for (int i = 0; i < C::STAGES; ++i)
-            mbar_init(smem_u32(&bars[warp][i]), 1);
+            mbar_init(smem_u32(&bars[warp][i]), 1 + (i == 0 && worker == p.stuck));
         fence_barrier_init();
     }
     __syncthreads();

@@ -242,3 +242,12 @@ def test_block_workspace_bytes():
     for bad in ((1, 2500, 1, 20, 5, 128), (1, 2560, 1, 3, 3, 64), (1, 2560, 1, 20, 5, 32),
                 (-1, 2560, 1, 20, 5, 128)):
         assert ws(*bad) == size_max
+
+
+@pytest.mark.parametrize("worker,timeout_us", [(-1, 1000), (0, 0), (0, -1), (0, 10 ** 7 + 1)])
+def test_inject_timeout_refuses_bad_workers_and_limits(worker, timeout_us):
+    cache, seqs = descriptors({})
+    rc = bl.lib().bitlinear_paged_attention_inject_timeout(
+        FAKE, 256, 3, 4, ctypes.addressof(cache), ctypes.addressof(seqs), 0.125, 0, 0, 2 * FAKE,
+        256, None, FAKE, BIG, None, worker, timeout_us)
+    assert rc == bl.BITLINEAR_ERR_ARG

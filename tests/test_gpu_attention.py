@@ -430,3 +430,45 @@ def test_prompts_on_many_streams_beside_decoding():
     for s, o in zip(steps, outs):
         s.check_attention(o[0])
         assert all(torch.equal(x.view(torch.int16), o[0].view(torch.int16)) for x in o)
+
+
+def timed_out(step, worker, **kw):
+    """A call in which `worker` waits in vain for 2 ms: a fault, every row of a head
+    complete or as it was, and the next call on the workspace right."""
+    y = torch.full((step.rows, step.hq, step.d), CANARY, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((step.rows, step.hq), CANARY, device="cuda")
+    ws = torch.empty(bl.bitlinear_workspace_bytes_attention(
+        step.rows, len(step.lens), step.hq, step.hkv, step.d), dtype=torch.uint8, device="cuda")
+    rc = bl.bitlinear_paged_attention_inject_timeout(
+        step.q, step.k_cache, step.v_cache, step.q_start, step.kv_len, step.table, worker, 2000,
+        y=y, lse=lse, workspace=ws, **kw)
+    assert rc == bl.BITLINEAR_OK
+    assert bl.bitlinear_get_fault() == (bl.BITLINEAR_ERR_TIMEOUT, 1)
+    want, tol, want_lse, lse_tol = step.attention()
+    kept = (y == CANARY).all(-1)
+    right = ((y.double() - want).abs() <= tol).all(-1)
+    assert (kept | right)[step.live].all() and kept[~step.live].all()
+    assert kept[step.live].any()
+    assert (lse[kept] == CANARY).all()
+    done = ~kept & step.live[:, None]
+    assert ((lse.double() - want_lse).abs() <= lse_tol)[done].all()
+    y.fill_(CANARY)
+    step.attend(y=y, lse=lse, workspace=ws, **kw)
+    step.check_attention(y, lse, CANARY)
+    assert bl.bitlinear_get_fault() == (bl.BITLINEAR_OK, 0)
+
+
+@pytest.mark.parametrize("worker", [0, 1, 5])
+@pytest.mark.parametrize("heads", [(8, 2, 128), (8, 2, 64)])
+def test_a_wait_that_runs_out_in_the_kernel_for_few_rows(heads, worker):
+    # single sequences' keys on many workers, and sequences whole on one
+    for lens in ([(1, 9000), (1, 40)], [(1, 30 + i) for i in range(300)]):
+        timed_out(Step(lens, heads, 16, seed=50, spare=2), worker, max_q_len=1)
+
+
+@pytest.mark.parametrize("worker", [0, 1, 7])
+@pytest.mark.parametrize("heads", [(20, 5, 128), (8, 2, 64)])
+def test_a_wait_that_runs_out_in_the_kernel_for_many_rows(heads, worker):
+    # neighbours wait for the worker's part of an item, in the kernel or behind it
+    for lens in ([(700, 900), (300, 1500)], [(130, 6000)], [(100, 130)] * 70):
+        timed_out(Step(lens, heads, 64, seed=51, spare=2), worker)
