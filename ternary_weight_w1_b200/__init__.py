@@ -569,19 +569,37 @@ def _ffn_width(packed, K: int) -> int:
 # A decode step makes these calls once per layer around kernels of a few
 # microseconds. Their common case is marshalled in C++ (csrc/fastcall.cpp); a
 # call that it does not take as plainly right goes through the checks below,
-# which find the error or make the call.
+# which find the error or make the call. So does every call where the extension
+# is missing or was built for another Python or torch.
 
 _fast_calls = None
+
+
+class _NoFastCalls:
+    """In the extension's place: takes no call."""
+
+    @staticmethod
+    def rope_append(*args):
+        return None
+
+    paged_attention = rope_append
 
 
 def _fast():
     global _fast_calls
     if _fast_calls is None:
         L = lib()
-        from . import _fastcall
-        address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
-        _fastcall.bind(address(L.bitlinear_rope_append), address(L.bitlinear_paged_attention))
-        _fast_calls = _fastcall
+        try:
+            from . import _fastcall
+            address = lambda f: ctypes.cast(f, ctypes.c_void_p).value  # noqa: E731
+            _fastcall.bind(address(L.bitlinear_rope_append), address(L.bitlinear_paged_attention))
+            _fast_calls = _fastcall
+        except ImportError as e:
+            import warnings
+            warnings.warn(f"the compiled marshalling of the attention calls does not load ({e}): "
+                          "they take 10 to 20 us longer on the host; build it with "
+                          "`python -m ternary_weight_w1_b200.build`", RuntimeWarning, stacklevel=3)
+            _fast_calls = _NoFastCalls
     return _fast_calls
 
 

@@ -6,7 +6,8 @@ The library is one CUDA translation unit (the kernels and the C ABI) plus
 the host packer and the packed-weight file reader and writer. cudart is
 linked statically so the library does not depend on which CUDA runtime the
 host process loaded first. Beside it stands _fastcall.so, a Python extension
-that marshals the paged-cache calls (csrc/fastcall.cpp, built with g++).
+that marshals the paged-cache calls (csrc/fastcall.cpp, built with g++); it is
+left out where torch or its headers are missing.
 """
 from __future__ import annotations
 
@@ -63,15 +64,22 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     return LIB
 
 
-def build_fastcall(force: bool = False, verbose: bool = False) -> str:
+def build_fastcall(force: bool = False, verbose: bool = False) -> str | None:
+    """The marshalling extension, or None without torch and its headers: the
+    library needs neither, and the binding works without the extension."""
     deps = (FAST_SOURCE, os.path.join(HERE, "..", "include", "bitlinear.h"))
     if not force and os.path.exists(FAST_LIB) and all(
             os.path.getmtime(FAST_LIB) >= os.path.getmtime(d) for d in deps):
         return FAST_LIB
     import sysconfig
 
-    import torch
+    try:
+        import torch
+    except ImportError:
+        return None
     root = os.path.dirname(torch.__file__)
+    if not os.path.isdir(os.path.join(root, "include")):
+        return None
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",

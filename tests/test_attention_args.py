@@ -1,6 +1,9 @@
 """The paged-cache operators refuse bad arguments on the host: every check here
 returns before the library touches CUDA."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -251,3 +254,44 @@ def test_inject_timeout_refuses_bad_workers_and_limits(worker, timeout_us):
         FAKE, 256, 3, 4, ctypes.addressof(cache), ctypes.addressof(seqs), 0.125, 0, 0, 2 * FAKE,
         256, None, FAKE, BIG, None, worker, timeout_us)
     assert rc == bl.BITLINEAR_ERR_ARG
+
+
+def without(modules, code):
+    """Runs `code` in a Python where importing any of `modules` fails."""
+    block = f"import sys; sys.modules.update(dict.fromkeys({modules!r}))\n"
+    return subprocess.run([sys.executable, "-c", block + code], capture_output=True, text=True,
+                          cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+
+def test_calls_work_without_the_compiled_marshalling():
+    # missing, or built for another Python or torch: the ctypes path takes every call
+    r = without(["ternary_weight_w1_b200._fastcall"], """
+import warnings
+import torch
+import ternary_weight_w1_b200 as bl
+c = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+i = lambda *s: torch.zeros(s, dtype=torch.int32)
+x = torch.zeros(3, 4, 64, dtype=torch.bfloat16)
+with warnings.catch_warnings(record=True) as seen:
+    warnings.simplefilter("always")
+    for call in (lambda: bl.bitlinear_paged_attention(x, c, c, i(2), i(1), i(1, 4)),
+                 lambda: bl.bitlinear_rope_append(x, x, x, c, c, i(2), i(1), i(1, 4), i(32))):
+        try:
+            call()
+        except ValueError as e:
+            print(e)
+print(len(seen), seen[0].category.__name__)
+""")
+    assert r.returncode == 0, r.stderr
+    *refusals, last = r.stdout.splitlines()
+    assert len(refusals) == 2 and all("CUDA tensor" in line for line in refusals)
+    assert last == "1 RuntimeWarning"              # said once
+
+
+def test_the_library_builds_without_torch():
+    r = without(["torch"], """
+from ternary_weight_w1_b200 import build
+print(build.build(), build.build_fastcall(force=True))
+""")
+    assert r.returncode == 0, r.stderr
+    assert r.stdout.split() == [bl.LIB_PATH, "None"]

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import ternary_weight_w1_b200 as bl
-from tests.paged_cases import Step
+from tests.paged_cases import Step, frequencies
 
 pytestmark = pytest.mark.gpu
 
@@ -472,3 +472,29 @@ def test_a_wait_that_runs_out_in_the_kernel_for_many_rows(heads, worker):
     # neighbours wait for the worker's part of an item, in the kernel or behind it
     for lens in ([(700, 900), (300, 1500)], [(130, 6000)], [(100, 130)] * 70):
         timed_out(Step(lens, heads, 64, seed=51, spare=2), worker)
+
+
+@pytest.mark.parametrize("lens", [[(1, 300), (1, 17)], [(70, 90), (1, 40)]])
+def test_python_and_compiled_marshalling_make_the_same_calls(lens, monkeypatch):
+    f = frequencies(64)
+    gain = torch.linspace(0.5, 1.5, 64, device="cuda")
+    got = []
+    for calls in (bl._fast(), bl._NoFastCalls):
+        monkeypatch.setattr(bl, "_fast_calls", calls)
+        step = Step(lens, (8, 2, 64), 16, seed=46, spare=1)
+        wide = torch.cat((step.q.flatten(1), step.k.flatten(1), step.v.flatten(1)), 1)
+        lse = torch.zeros((step.rows, 8), device="cuda")
+        q = step.append(f, q=wide[:, :512], k=wide[:, 512:640], v=wide[:, 640:].view(-1, 2, 64),
+                        q_gain=gain, eps=1e-5, interleaved=True)
+        y = step.attend(q=q, lse=lse, window=50, scale=0.2, max_q_len=70)
+        z = step.attend(q=q.view(-1, 8, 64), stream=torch.cuda.Stream())
+        torch.cuda.synchronize()
+        got.append([t.view(torch.int16)[step.live] for t in (q, y, z, lse)] +
+                   [c.view(torch.int16) for c in (step.k_cache, step.v_cache)])
+        with pytest.raises(ValueError, match="rows"):
+            step.attend(q=q, y=y[:1])
+        with pytest.raises(bl.BitLinearError):
+            step.attend(q=q, scale=-1.0)
+    assert bl._fast().__name__ == "_NoFastCalls"
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
