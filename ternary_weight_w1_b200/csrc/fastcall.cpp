@@ -126,7 +126,18 @@ void *stream_of(PyObject *o, int device)
     return o == Py_None ? c10::cuda::getCurrentCUDAStream(device).stream() : PyLong_AsVoidPtr(o);
 }
 
-PyObject *status(int rc) { return PyLong_FromLong(rc); }
+// The status of a library call, which runs without the interpreter's lock: a launch
+// waits while the stream's queue is full, and what empties the queue may need a Python
+// thread (a host callback). The caller holds the tensors.
+template <typename F>
+PyObject *status(F call)
+{
+    int rc;
+    Py_BEGIN_ALLOW_THREADS;
+    rc = call();
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(rc);
+}
 
 // q, k, v, k_cache, v_cache, q_start, kv_len, page_table, inv_freq, q_out,
 // q_gain, k_gain, eps, interleaved, stream
@@ -149,15 +160,18 @@ PyObject *rope_append(PyObject *, PyObject *const *a, Py_ssize_t n)
         const void *kg = in.optional(a[11], at::kFloat, D);
         const double eps = PyFloat_AsDouble(a[12]);
         const int interleaved = PyObject_IsTrue(a[13]);
+        void *const stream = stream_of(a[14], in.device);
         if (!in.ok || PyErr_Occurred()) {
             PyErr_Clear();
             Py_RETURN_NONE;
         }
-        return status(g_rope_append(q.p, q.stride, k.p, k.stride, v.p, v.stride, q.rows, q.heads,
-                                    &p.cache, &p.seqs, static_cast<const float *>(f->data_ptr()),
-                                    interleaved, static_cast<const float *>(qg),
-                                    static_cast<const float *>(kg), static_cast<float>(eps), out.p,
-                                    out.stride, stream_of(a[14], in.device)));
+        const auto *freq = static_cast<const float *>(f->data_ptr());
+        return status([&] {
+            return g_rope_append(q.p, q.stride, k.p, k.stride, v.p, v.stride, q.rows, q.heads,
+                                 &p.cache, &p.seqs, freq, interleaved,
+                                 static_cast<const float *>(qg), static_cast<const float *>(kg),
+                                 static_cast<float>(eps), out.p, out.stride, stream);
+        });
     } catch (const std::exception &) {
         Py_RETURN_NONE;
     }
@@ -184,14 +198,19 @@ PyObject *paged_attention(PyObject *, PyObject *const *a, Py_ssize_t n)
             a[6] == Py_None ? 1.0 / std::sqrt(static_cast<double>(D)) : PyFloat_AsDouble(a[6]);
         const int64_t window = PyLong_AsLongLong(a[7]);
         const int64_t max_q = a[8] == Py_None ? 0 : PyLong_AsLongLong(a[8]);
+        void *const stream = stream_of(a[12], in.device);
         if (!in.ok || PyErr_Occurred()) {
             PyErr_Clear();
             Py_RETURN_NONE;
         }
-        return status(g_paged_attention(
-            q.p, q.stride, q.rows, q.heads, &p.cache, &p.seqs, static_cast<float>(scale), window,
-            max_q, y.p, y.stride, lse == nullptr ? nullptr : static_cast<float *>(lse->data_ptr()),
-            ws->data_ptr(), static_cast<size_t>(ws->numel()), stream_of(a[12], in.device)));
+        float *const lse_p = lse == nullptr ? nullptr : static_cast<float *>(lse->data_ptr());
+        void *const ws_p = ws->data_ptr();
+        const size_t ws_bytes = static_cast<size_t>(ws->numel());
+        return status([&] {
+            return g_paged_attention(q.p, q.stride, q.rows, q.heads, &p.cache, &p.seqs,
+                                     static_cast<float>(scale), window, max_q, y.p, y.stride, lse_p,
+                                     ws_p, ws_bytes, stream);
+        });
     } catch (const std::exception &) {
         Py_RETURN_NONE;
     }

@@ -498,3 +498,50 @@ def test_python_and_compiled_marshalling_make_the_same_calls(lens, monkeypatch):
     assert bl._fast().__name__ == "_NoFastCalls"
     for a, b in zip(*got):
         assert torch.equal(a, b)
+
+
+def test_other_python_threads_run_during_a_call(tmp_path):
+    # the extension's calls bound to a function that waits until another thread of
+    # the interpreter has run (two seconds at most)
+    import ctypes
+    import subprocess
+    import threading
+    src = tmp_path / "wait.c"
+    src.write_text("""
+#include <time.h>
+static volatile int go, in;
+int inside(void) { return in; }
+void set(int v) { go = v; in = 0; }
+int call(void) {
+    struct timespec t = {0, 1000000};
+    in = 1;
+    for (int i = 0; i < 2000 && !go; ++i) nanosleep(&t, 0);
+    return go ? 0 : 2;
+}
+""")
+    subprocess.run(["gcc", "-O1", "-shared", "-fPIC", str(src), "-o", str(tmp_path / "wait.so")],
+                   check=True)
+    wait = ctypes.CDLL(str(tmp_path / "wait.so"))
+    address = ctypes.cast(wait.call, ctypes.c_void_p).value
+    L, fast = bl.lib(), bl._fast()
+    step, f = Step([(1, 30)], (8, 2, 64), 16, seed=47), frequencies(64)
+    real = [ctypes.cast(n, ctypes.c_void_p).value
+            for n in (L.bitlinear_rope_append, L.bitlinear_paged_attention)]
+    fast.bind(address, address)
+    try:
+        for call in (lambda: step.append(f), step.attend):
+            wait.set(0)
+
+            def other():
+                while not wait.inside():
+                    pass
+                wait.set(1)
+
+            thread = threading.Thread(target=other, daemon=True)
+            thread.start()
+            call()                                     # raises when the other never ran
+            thread.join(timeout=10)
+            assert not thread.is_alive()
+    finally:
+        fast.bind(*real)
+    step.check_attention(step.attend())
