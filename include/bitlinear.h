@@ -555,7 +555,8 @@ typedef struct {
  *                  queries and of the keys, each NULL for none
  *   norm_eps [in]  finite and > 0 when a gain is given
  *   q_out_dev [out] the rotated queries, q_out_stride likewise; may be q_dev
- *                  (with the same stride)
+ *                  (with the same stride), but shares no other element with the
+ *                  rows of q, k and v (BITLINEAR_ERR_ARG)
  * Everything between load and store is fp32, rounded once to bf16. Tokens at
  * negative positions are skipped. Two rows must not have the same place in the
  * cache. */
@@ -592,7 +593,8 @@ size_t bitlinear_workspace_bytes_attention(int64_t tokens, int64_t seqs,
  *                  value costs speed, never correctness
  *   y_dev, y_stride [out] rows of q_heads * head_dim bf16, 16-byte aligned,
  *                  stride a multiple of 8. Rows that see no key are zero; rows
- *                  of no sequence stay as they are. May not overlap q_dev
+ *                  of no sequence stay as they are. Shares no element with
+ *                  the rows of q_dev (BITLINEAR_ERR_ARG)
  *   lse_dev_or_null [out, optional] [tokens][q_heads] fp32: the natural
  *                  logarithm of sum_j exp(scale * q_t . k_j), -inf for a row
  *                  without keys

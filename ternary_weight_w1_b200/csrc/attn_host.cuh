@@ -3,6 +3,8 @@
 // helpers; the C ABI functions are declared in include/bitlinear.h.
 #pragma once
 
+#include "row_set.cuh"
+
 namespace {
 
 constexpr int kAttnMaxGrid = 192;                    // SMs that a launch uses at most
@@ -358,6 +360,13 @@ extern "C" int bitlinear_rope_append(const void *q_dev, int64_t q_stride, const 
     }
     if (!aligned(inv_freq_dev, 4) || !aligned(q_gain_dev, 4) || !aligned(k_gain_dev, 4))
         return BITLINEAR_ERR_ALIGN;
+    // queries rotated where they stand are read and written by the same threads
+    const RowSet out{q_out_dev, q_out_stride, q_heads * D};
+    const bool in_place = q_out_dev == q_dev && (q_out_stride == q_stride || tokens == 1);
+    if ((!in_place && share_memory(out, RowSet{q_dev, q_stride, q_heads * D}, tokens)) ||
+        share_memory(out, RowSet{k_dev, k_stride, cache->kv_heads * D}, tokens) ||
+        share_memory(out, RowSet{v_dev, v_stride, cache->kv_heads * D}, tokens))
+        return BITLINEAR_ERR_ARG;
     DeviceInfo *dev = nullptr;
     rc = current_device(&dev);
     if (rc != BITLINEAR_OK)
@@ -430,6 +439,9 @@ int paged_attention_impl(const void *q_dev, int64_t q_stride, int64_t tokens, in
         return BITLINEAR_ERR_WORKSPACE;
     if (!aligned(workspace_dev, 256))
         return BITLINEAR_ERR_ALIGN;
+    if (share_memory(RowSet{y_dev, y_stride, q_heads * D}, RowSet{q_dev, q_stride, q_heads * D},
+                     tokens))
+        return BITLINEAR_ERR_ARG;
     DeviceInfo *dev = nullptr;
     rc = current_device(&dev);
     if (rc != BITLINEAR_OK)

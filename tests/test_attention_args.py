@@ -295,3 +295,19 @@ print(build.build(), build.build_fastcall(force=True))
 """)
     assert r.returncode == 0, r.stderr
     assert r.stdout.split() == [bl.LIB_PATH, "None"]
+
+
+@pytest.mark.parametrize("call,kw", [
+    (attend, dict()),                                     # y is q
+    (attend, dict(T=1)),
+    (attend, dict(y=FAKE + 16)),
+    (attend, dict(y=FAKE + 2 * 512)),                     # q's last row
+    (attend, dict(qs=512, ys=512, y=FAKE + 2 * 240)),     # a part of a wide buffer, 16 too near
+    (attend, dict(qs=512, ys=256, y=FAKE + 2 * 768)),
+    (append, dict(kk=2 * FAKE, vv=3 * FAKE, os=512)),     # in place, with another stride
+    (append, dict(kk=2 * FAKE, vv=3 * FAKE, out=FAKE + 512)),
+    (append, dict(kk=2 * FAKE, vv=3 * FAKE, out=2 * FAKE + 16)),
+    (append, dict(kk=2 * FAKE, vv=3 * FAKE, out=3 * FAKE - 512)),
+])
+def test_outputs_that_share_memory_with_inputs(call, kw):
+    assert call(**kw) == bl.BITLINEAR_ERR_ARG

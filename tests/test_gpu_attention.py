@@ -545,3 +545,32 @@ int call(void) {
     finally:
         fast.bind(*real)
     step.check_attention(step.attend())
+
+
+def test_queries_and_outputs_side_by_side_and_on_top_of_each_other():
+    step = Step([(1, 77), (40, 90)], (4, 2, 64), 16, seed=48)
+    wide = torch.full((step.rows, 768), CANARY, dtype=torch.bfloat16, device="cuda")
+    wide[:, 256:512] = step.q.flatten(1)
+    for at in (0, 512):                                # their ranges overlap, no element does
+        step.check_attention(step.attend(q=wide[:, 256:512], y=wide[:, at:at + 256]))
+        assert torch.equal(wide[:, 256:512], step.q.flatten(1))
+    for y in (wide[:, 256:512], wide[:, 248:504], wide[:, 264:520], wide[:, 8:264]):
+        with pytest.raises(bl.BitLinearError) as e:
+            step.attend(q=wide[:, 256:512], y=y)
+        assert e.value.status == bl.BITLINEAR_ERR_ARG
+    # the append's queries: q, k and v in one buffer, the output over one of them
+    flat = torch.full((step.rows * 776,), CANARY, dtype=torch.bfloat16, device="cuda")
+    fused = flat[:step.rows * 768].view(step.rows, 768)
+    fused[:, :512] = torch.cat((step.q.flatten(1), step.k.flatten(1), step.v.flatten(1)), 1)
+    kept = flat.clone()
+    parts = dict(q=fused[:, :256], k=fused[:, 256:384], v=fused[:, 384:512])
+    for out in (fused[:, 8:264], fused[:, 264:520], fused[:, 504:760],
+                flat.as_strided((step.rows, 256), (776, 1))):
+        with pytest.raises(bl.BitLinearError) as e:
+            step.append(frequencies(64), q_out=out, **parts)
+        assert e.value.status == bl.BITLINEAR_ERR_ARG
+    assert torch.equal(flat, kept)
+    step.append(frequencies(64), q_out=fused[:, 512:], **parts)
+    want, tol = step.rotated(step.q, frequencies(64))
+    assert ((fused[:, 512:].reshape(want.shape).double() - want).abs() <= tol).all()
+    assert torch.equal(fused[:, :512], kept[:step.rows * 768].view(step.rows, 768)[:, :512])
