@@ -24,7 +24,8 @@
 // held down by power, but 20% slower on windowed prompts of 64 channels); every
 // pair of exponentials on the special-function unit 4% slower, every second on
 // the multiply-add pipe 4% slower. 4096 rows behind 28672 keys, 64 heads on 8:
-// 3.7 to 4.5 ms, 920 to 1110 TFLOP/s by the clock that power leaves.
+// 4.0 to 4.5 ms, 920 to 1030 TFLOP/s, in calls back to back, by the clock that power
+// leaves (3.7 ms on its own).
 //
 // Items that are split into up to four parts, as most split ones are, are joined
 // here: a worker computes the part of the item that began before its run first
@@ -36,8 +37,9 @@
 // clears them. Runs are numbered from the last block to the first, so that a block
 // waits only for blocks of a lower number. The GPU starts blocks in the order of
 // their numbers: what is waited for runs already or is done, however few SMs other
-// work leaves to the launch. (Leaving every part to a kernel of its own took 18 us
-// of 60 at 2048 tokens of the 2B layer.)
+// work leaves to the launch. (The other numbering, in which the waiting blocks start
+// first, is 0.5 us of 46 faster at 2048 tokens of the 2B layer. Leaving every part to a
+// kernel of its own took 18 us of 60 there.)
 //
 // One persistent block per SM. Warps 0-7 and 8-15 compute the halves' softmax,
 // warp 16 fetches keys and values through a ring of tiles, and the next item's

@@ -171,7 +171,8 @@ constexpr int kRowsKernelMax = 32;                   // rows of the rows kernel'
 // channels 78 / 117 us, 20 rows on each of 5 of 128 channels 114 / 74 us, 32 rows
 // 119 / 74 us, 16 rows 70 / 73 us. Two row tiles of 128 channels are more than a
 // thread's registers hold, and half an item of the chunk kernel keeps up with HBM
-// there. (Four sequences of 32 rows of 64 channels are 46 / 37.)
+// there. The rule looks at the rows alone, so it is not the best one for few
+// sequences: four of 32 rows of 64 channels are 46 / 37.
 constexpr int64_t rows_kernel_rows(int64_t head_dim) { return head_dim == 64 ? 32 : 16; }
 
 // Workspace: the parts of the rows kernel, then those of the chunk kernel, which
