@@ -127,3 +127,43 @@ def test_captured_decode_step_of_the_2b_layer(T):
         graph.replay()
         want = call(two, torch.empty_like(y))
         assert torch.equal(y.view(torch.int16), want.view(torch.int16))
+
+
+def test_blocks_on_two_streams_at_once():
+    # a prompt's and a decode step's, each with what the call allocates
+    K, heads = LAYOUTS[0]
+    proj, gains = layer(K, heads)
+    f = frequencies(heads[2])
+    work = []
+    for i, lens in enumerate(([(300, 300), (90, 500)], [(1, 60 * n) for n in range(1, 12)])):
+        one, two = steps(lens, heads, 64, 20 + i, spare=0)
+        x = torch.from_numpy(workloads.activations_f32(one.rows, K, 6 + i)).cuda()
+        work.append((one, two, x.to(torch.bfloat16)))
+
+    def call(step, x, stream=None):
+        return bl.bitlinear_attn_forward(x, *proj, heads[0], step.k_cache, step.v_cache,
+                                         step.q_start, step.kv_len, step.table, f,
+                                         gains=gains[:4], stream=stream)
+
+    want = [call(two, x) for _, two, x in work]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[], []]
+    for _ in range(8):
+        for i, (one, _, x) in enumerate(work):
+            outs[i].append(call(one, x, streams[i]))
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert all(torch.equal(y.view(torch.int16), w.view(torch.int16)) for y in o)
+
+
+def test_a_block_of_no_rows():
+    K, heads = LAYOUTS[0]
+    proj, _ = layer(K, heads)
+    step = Step([(0, 30)], heads, 64, seed=9)
+    kept = step.k_cache.clone()
+    y = bl.bitlinear_attn_forward(torch.empty((0, K), dtype=torch.bfloat16, device="cuda"), *proj,
+                                  heads[0], step.k_cache, step.v_cache, step.q_start, step.kv_len,
+                                  step.table, frequencies(heads[2]))
+    assert y.shape == (0, K)
+    assert torch.equal(step.k_cache.view(torch.int16), kept.view(torch.int16))
