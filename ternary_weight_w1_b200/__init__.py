@@ -642,7 +642,7 @@ def _new(t, stream, shape=None, dtype=None):
     import torch
     out = torch.empty(t.shape if shape is None else shape,
                       dtype=t.dtype if dtype is None else dtype, device=t.device)
-    if stream is not None and stream != torch.cuda.current_stream():
+    if stream is not None and out.is_cuda and stream != torch.cuda.current_stream():
         stream.wait_stream(torch.cuda.current_stream())   # what used the memory before
         out.record_stream(stream)
     return out

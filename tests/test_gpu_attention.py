@@ -574,3 +574,11 @@ def test_queries_and_outputs_side_by_side_and_on_top_of_each_other():
     want, tol = step.rotated(step.q, frequencies(64))
     assert ((fused[:, 512:].reshape(want.shape).double() - want).abs() <= tol).all()
     assert torch.equal(fused[:, :512], kept[:step.rows * 768].view(step.rows, 768)[:, :512])
+
+
+def test_host_tensors_are_named_on_another_stream_too():
+    step, stream = Step([(1, 30)], (8, 2, 64), 16, seed=49), torch.cuda.Stream()
+    for call in (lambda q: step.attend(q=q, stream=stream),
+                 lambda q: step.append(frequencies(64), q=q, stream=stream)):
+        with pytest.raises(ValueError, match="CUDA tensor"):
+            call(step.q.cpu())
